@@ -86,6 +86,23 @@ pa_status_t pa_bm_add_sequence(pa_block_manager* bm, int64_t seq_id, const int64
 pa_status_t pa_bm_append_slots(pa_block_manager* bm, const int64_t* seq_ids, const int64_t* token_ids, int32_t n,
                                int64_t* slots_out, int32_t* cow_out, int32_t* num_cow);
 
+/*
+ * Cut a sequence to its first new_len positions (0 <= new_len <= its length):
+ * blocks past them lose this sequence's count.  After a drafting step, whose
+ * positions were appended without token ids (their order is not the text's):
+ * the accepted ones were moved to the front (pa_commit_tree), the rest goes,
+ * and token_ids [num_token_ids] (may be NULL with 0) are the ids of the last
+ * num_token_ids kept positions, which were appended without.  When every
+ * position before them is known, the blocks they fill are added to the prefix
+ * cache and later appends with ids go on where these end; else they are not
+ * used.  PA_ERR_INVALID when more ids are given than kept positions were
+ * appended without.  A block that the cut leaves partly filled is taken out of
+ * the prefix cache; cutting inside an earlier block whose ids were known makes
+ * the ids of that block unknown.
+ */
+pa_status_t pa_bm_truncate(pa_block_manager* bm, int64_t seq_id, int32_t new_len, const int64_t* token_ids,
+                           int32_t num_token_ids);
+
 /* Child shares every block of parent (same length). */
 pa_status_t pa_bm_fork(pa_block_manager* bm, int64_t parent_id, int64_t child_id);
 

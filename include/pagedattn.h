@@ -90,10 +90,11 @@ typedef enum {
 
 /* Bits of the device error word. */
 enum {
-  PA_DEVERR_SLOT = 1u,       /* write_kv: slot >= num_blocks * block_size (row skipped) */
+  PA_DEVERR_SLOT = 1u,       /* write_kv, rope_append: slot >= num_blocks * block_size (row skipped) */
   PA_DEVERR_BLOCK = 2u,      /* decode: block id outside [0, num_blocks) (tile skipped) */
   PA_DEVERR_CONTEXT = 4u,    /* decode: context_lens[b] < 0 or > max_blocks_per_seq * block_size,
-                                or > max_context_len in split-K (length clamped) */
+                                or > max_context_len in split-K (length clamped); decode_tree,
+                                commit_tree: lengths or a path that do not fit (sequence skipped) */
   PA_DEVERR_TIMEOUT = 8u,    /* a bounded wait on a tile load gave up (output row not written) */
   PA_DEVERR_LAYOUT = 16u     /* prefill: shared memory was not 1024-byte aligned (tile not computed) */
 };
@@ -308,6 +309,144 @@ pa_status_t pa_decode_cascade(const void* q, const void* k_cache, const void* v_
 size_t pa_decode_cascade_workspace_size(int32_t batch, int32_t num_q_heads, int32_t head_dim,
                                         int32_t max_context_len, int32_t prefix_len, int32_t partition_tokens,
                                         int32_t num_kv_heads);
+
+/*
+ * pa_qk_norm_rope -- norm and rotate one step's queries and keys, per head.
+ *   q: num_tokens rows of [num_q_heads][head_dim], k: of [num_kv_heads]
+ *   [head_dim]; row i starts q_stride (k_stride) elements after row i - 1, so
+ *   that both may be slices of a fused projection's output.  For each head
+ *   vector x, in fp32 with one rounding at the end:
+ *     norm      y = x / sqrt(mean(x^2) + eps) * weight   (q_weight for q,
+ *               k_weight for k: fp32 [head_dim], or NULL for no norm)
+ *     rotation  of the first rotary_dim elements, by the angle
+ *               t_i = positions[token] * inv_freq[i], i < rotary_dim / 2
+ *               (inv_freq: fp32; t_i is reduced in 64 bits):
+ *               (a, b) -> (a cos t_i - b sin t_i, b cos t_i + a sin t_i)
+ *               for the pair of elements (i, i + rotary_dim / 2), or
+ *               (2 i, 2 i + 1) when interleaved != 0.  Elements from
+ *               rotary_dim on are not rotated; rotary_dim = 0: norm only
+ *               (positions and inv_freq may be NULL).
+ *   q_out, k_out: as q and k, with their own strides; q_out == q and k_out ==
+ *   k with equal strides work in place (any other overlap is undefined).  The
+ *   results are pa_decode_step's q and k_new, or pa_prefill's.
+ *   positions: int32 [num_tokens], any value.
+ *   Supported: head_dim in {64, 128, 256}; rotary_dim a multiple of 16 in
+ *   [0, head_dim]; any head counts (num_q_heads need not divide by
+ *   num_kv_heads here), num_q_heads + 2 num_kv_heads <= 65535.
+ *   Returns PA_ERR_INVALID for null or misaligned pointers (rows 16-byte:
+ *   strides are multiples of 16 bytes; weights 16-byte, positions and
+ *   inv_freq 4-byte), bad sizes, an output stride shorter than a row, a
+ *   negative or non-finite eps.  One launch.
+ *   Passages: nano-vllm (ovshake) README, "Key Concepts Explained: KV Cache"
+ *   (each step computes K and V for the new tokens only); the pages print no
+ *   formula of the rotation or the norm.
+ */
+pa_status_t pa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* q_weight,
+                            const float* k_weight, float eps, const float* inv_freq, int32_t rotary_dim,
+                            int32_t interleaved, const int32_t* positions, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, pa_dtype_t dtype, pa_stream_t stream);
+
+/*
+ * pa_rope_append -- norm and rotate one step's queries and keys and append
+ * keys and values to the paged cache, in one pass.
+ *   q and k are treated as in pa_qk_norm_rope; the rotated keys go straight to
+ *   the cache, and v's rows (v_stride apart) are copied there bit for bit:
+ *     k_cache[s / bs][h][s % bs][:] = rotated k[i][h][:],
+ *     v_cache[s / bs][h][s % bs][:] = v[i][h][:],   s = slot_mapping[i].
+ *   q_out: [num_tokens][num_q_heads][head_dim], contiguous; q_out == q works
+ *   in place when q_stride is num_q_heads * head_dim.
+ *   slot_mapping[i] < 0 marks a padding token: neither its q_out row nor the
+ *   cache is written.  A slot >= num_blocks * block_size sets PA_DEVERR_SLOT;
+ *   its K and V rows are skipped, its q_out row is written.  Two tokens with
+ *   the same slot in one call: which one lands is undefined.
+ *   The attention that follows is a call over the cache (pa_decode_splitk,
+ *   pa_decode_multi, pa_decode_tree, pa_prefill with k_new = NULL).
+ *   Supported as pa_qk_norm_rope; block_size any positive number, as
+ *   pa_write_kv.  One launch.
+ */
+pa_status_t pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const float* q_weight, const float* k_weight, float eps,
+                           const float* inv_freq, int32_t rotary_dim, int32_t interleaved, const int32_t* positions,
+                           const int64_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, void* q_out, void* k_cache, void* v_cache,
+                           int32_t num_blocks, int32_t block_size, pa_dtype_t dtype, pa_stream_t stream);
+
+/*
+ * pa_decode_tree -- attention of a tree of drafted tokens over the cache
+ * (the verify step of tree speculative decoding).
+ *   q, out: [batch][tree_len][num_q_heads][head_dim].  Sequence b's tree has
+ *   n = tree_lens[b] nodes (tree_len for every sequence when tree_lens is
+ *   NULL), whose keys and values are already in the cache, as the last n of
+ *   its L = context_lens[b] positions: node j at position base + j, base =
+ *   L - n (append them with pa_rope_append or pa_write_kv first).
+ *   tree_mask: int64 words, node j of sequence b at [b * mask_stride + j]; bit
+ *   i of a node's word says that it attends node i (its ancestors and itself;
+ *   bits from n on are ignored).  mask_stride: tree_len or more, or 0 when
+ *   every sequence drafts the same tree.  With depth_j the number of nodes
+ *   that j attends besides itself, node j stands at the logical position
+ *   p_j = base + depth_j and attends
+ *     every position t < base with t > p_j - window, and
+ *     every node i of its mask with p_i > p_j - window
+ *   (window <= 0: no bound); scores, softcap and softmax as pa_decode.  A
+ *   row that attends nothing is zero, as are the rows of nodes j >= n.  L = 0
+ *   marks an empty (padding) sequence: zero rows.  What stands in the cache
+ *   at a place that a row does not attend, NaN and infinities included,
+ *   does not reach that row.
+ *   tree_lens[b] outside [0, tree_len], L < n, L < 0 or L above
+ *   max_context_len or the table's length sets PA_DEVERR_CONTEXT and gives
+ *   zero rows.
+ *   A chain of drafts (word j = the bits 0 .. j) is pa_decode_multi.
+ *   1 <= tree_len <= 64 (PA_ERR_UNSUPPORTED above).  bf16 runs on the tensor
+ *   cores, fp32 on CUDA cores.
+ *   workspace: for bf16, device memory of at least
+ *   pa_decode_tree_workspace_size() bytes, 16-byte aligned, scratch within a
+ *   call; it needs no zeroing.  The first 256 KiB (pa_decode_splitk's counter
+ *   region) are left alone, so that a workspace may serve this call and
+ *   pa_decode_splitk's family.  Calls that share a workspace must be ordered
+ *   on one stream.  fp32: none (workspace may be NULL).
+ *   Passages: nano-vllm (ovshake) README, "Features" (speculative decoding)
+ *   and the speculative-decoding command line (--num-speculative-tokens);
+ *   attention over the cache as in "Key Concepts Explained: KV Cache".
+ */
+pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                           const int32_t* context_lens, const int32_t* tree_lens, const int64_t* tree_mask,
+                           int64_t mask_stride, int32_t batch, int32_t tree_len, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                           int32_t num_blocks, float scale, float softcap, int32_t window, void* out,
+                           pa_dtype_t dtype, int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                           pa_stream_t stream);
+size_t pa_decode_tree_workspace_size(int32_t batch, int32_t tree_len, int32_t num_q_heads, int32_t head_dim,
+                                     int32_t max_context_len, int32_t num_kv_heads);
+
+/*
+ * pa_commit_tree -- keep the accepted path of a drafted tree: move its rows to
+ * the positions they end up in, in the caches of all layers.
+ *   accepted: int32 [batch][max_accept]; the first a = accept_lens[b] entries
+ *   are node numbers of sequence b's tree in path order, strictly increasing
+ *   (a tree numbers a child after its parent).  Node accepted[b][i], at
+ *   position base + accepted[b][i], becomes position base + i, i < a, with
+ *   base = context_lens[b] - n and n as in pa_decode_tree; the rows of the
+ *   other nodes are left as they are.  new_lens[b] = base + a (may be NULL;
+ *   must not be context_lens, which other CTAs still read).  The copies are
+ *   bit-exact.
+ *   k_cache, v_cache: [num_layers][num_blocks][num_kv_heads][block_size]
+ *   [head_dim], one block table for all layers; num_layers = 1 for the cache
+ *   of one layer.
+ *   The blocks that hold a sequence's tree must not be shared with another
+ *   sequence.  context_lens[b] = 0: an empty (padding) sequence, new length
+ *   0.  Lengths as in pa_decode_tree that do not fit, a outside [0,
+ *   min(max_accept, n)] or a path that is not strictly increasing within
+ *   [0, n) sets PA_DEVERR_CONTEXT: nothing of the sequence moves and its new
+ *   length is the old one.  A block id outside the pool sets PA_DEVERR_BLOCK
+ *   and its row is skipped.  One launch.
+ *   Passages: nano-vllm (ovshake) README, "Features" (speculative decoding).
+ */
+pa_status_t pa_commit_tree(void* k_cache, void* v_cache, int32_t num_layers, const int32_t* block_tables,
+                           const int32_t* context_lens, const int32_t* tree_lens, int32_t tree_len,
+                           const int32_t* accepted, int32_t max_accept, const int32_t* accept_lens, int32_t batch,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                           int32_t num_blocks, int32_t* new_lens, pa_dtype_t dtype, pa_stream_t stream);
 
 /*
  * pa_decode_splitk_noalloc -- pa_decode_splitk for callers that cannot allocate

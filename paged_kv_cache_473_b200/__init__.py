@@ -1,4 +1,5 @@
-"""B200 (sm_100a) paged KV cache: KV append and paged decode attention.
+"""B200 (sm_100a) paged KV cache: KV append and paged decode attention, and
+the steps around them that a drafting engine runs on the same cache.
 
 The compute lives in ``libpagedattn.so`` (C ABI, include/pagedattn.h); this
 package is its Python binding plus seeded synthetic batch generators
@@ -9,6 +10,7 @@ package, or only its input generators, maps no GPU code.
 
 from ._binding import (  # noqa: F401
     BlockManager,
+    commit_tree,
     copy_blocks,
     DEVERR_BLOCK,
     DEVERR_CONTEXT,
@@ -27,12 +29,16 @@ from ._binding import (  # noqa: F401
     decode_step,
     decode_splitk_partition,
     decode_splitk_workspace_size,
+    decode_tree,
+    decode_tree_workspace_size,
     check_bounded_wait,
     device_errors,
     error_string,
     last_decode_schedule,
     last_launch_count,
     prefill,
+    qk_norm_rope,
+    rope_append,
     write_kv,
 )
 
@@ -64,6 +70,11 @@ __all__ = [
     "error_string",
     "last_decode_schedule",
     "last_launch_count",
+    "decode_tree",
+    "decode_tree_workspace_size",
+    "commit_tree",
     "prefill",
+    "qk_norm_rope",
+    "rope_append",
     "PagedAttnError",
 ]

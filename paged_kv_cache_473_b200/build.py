@@ -1,4 +1,7 @@
-"""Build the sm_100a shared library ``libpagedattn.so`` in-tree with nvcc."""
+"""Build the sm_100a shared library ``libpagedattn.so`` in-tree with nvcc.
+
+Each translation unit is compiled to an object of its own, the units at the
+same time, and only those whose sources changed; then they are linked."""
 
 from __future__ import annotations
 
@@ -7,14 +10,17 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libpagedattn.so")
 MAIN = os.path.join(CSRC, "pagedattn.cu")
-# Translation units: the kernels and their C ABI, and the host block manager.
-UNITS = [MAIN, os.path.join(CSRC, "block_manager.cpp")]
+# Translation units: the append, decode and prefill kernels and their C ABI,
+# the drafting step's operators and theirs, and the host block manager.
+UNITS = [MAIN, os.path.join(CSRC, "tree_ops.cu"), os.path.join(CSRC, "block_manager.cpp")]
+OBJ_DIR = os.path.join(PKG, "_build")
 
 NVCC_FLAGS = [
     "-gencode",
@@ -24,7 +30,6 @@ NVCC_FLAGS = [
     "-std=c++17",
     "-Xcompiler",
     "-fPIC",
-    "-shared",
 ]
 
 
@@ -47,11 +52,43 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+def _object(unit: str) -> str:
+    return os.path.join(OBJ_DIR, os.path.basename(unit) + ".o")
+
+
+def _fresh(obj: str) -> bool:
+    """Whether an object is newer than every source its compiler read."""
+    if not (os.path.exists(obj) and os.path.exists(obj + ".d")):
+        return False
+    with open(obj + ".d") as f:
+        deps = f.read().replace("\\\n", " ").split(":", 1)[1].split()
+    t = os.path.getmtime(obj)
+    return all(os.path.exists(d) and os.path.getmtime(d) <= t for d in deps)
+
+
+def _compile(unit: str, force: bool, verbose: bool, extra_flags) -> str:
+    obj = _object(unit)
+    if not force and _fresh(obj):
+        return obj
+    tmp = f"{obj}.tmp{os.getpid()}"
+    cmd = [_nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-MMD", "-MF", tmp + ".d",
+           "-c", "-o", tmp, unit]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp + ".d", obj + ".d")
+    os.replace(tmp, obj)
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if not force and up_to_date():
         return LIB
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with ThreadPoolExecutor(len(UNITS)) as pool:
+        objs = list(pool.map(lambda u: _compile(u, force, verbose, extra_flags), UNITS))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-o", tmp, *UNITS]
+    cmd = [_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)

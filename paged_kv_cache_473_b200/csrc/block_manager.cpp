@@ -41,11 +41,15 @@ struct Block {
 struct Seq {
   std::vector<int32_t> blocks;
   int32_t len = 0;
-  // Prefix-cache chaining: the hash of the last full block, whether every
-  // token so far is known, and the token ids of the partly filled last block.
-  uint64_t last_full_hash = kNoHash;
-  bool tokens_known = true;
+  // Prefix-cache chaining: how many leading positions have known token ids,
+  // the hash of each full block of those, and the ids behind the last one
+  // (known - hashes.size() * block_size of them).  Ids are added only while
+  // every position is known (known == len).
+  int32_t known = 0;
+  std::vector<uint64_t> hashes;
   std::vector<int64_t> tail_tokens;
+
+  uint64_t last_full_hash() const { return hashes.empty() ? kNoHash : hashes.back(); }
 };
 
 }  // namespace
@@ -117,6 +121,24 @@ struct pa_block_manager {
         free_list.push_back(id);
         in_free[id] = 1;
       }
+    }
+  }
+
+  // The next unknown position of a sequence holds this token: a block that is
+  // filled with known tokens is registered in the prefix cache.  Out of host
+  // memory, the ids of that block (and so of what follows) stay unknown.
+  void learn(Seq& s, int64_t token) {
+    try {
+      s.tail_tokens.push_back(token);
+      ++s.known;
+      if (s.known % block_size != 0) return;
+      const uint64_t parent = s.last_full_hash(), h = block_hash(parent, s.tail_tokens.data(), block_size);
+      s.hashes.push_back(h);
+      register_full(s.blocks[s.known / block_size - 1], parent, s.tail_tokens.data(), h);
+      s.tail_tokens.clear();
+    } catch (...) {
+      s.tail_tokens.clear();
+      s.known = (int32_t)s.hashes.size() * block_size;
     }
   }
 
@@ -206,12 +228,14 @@ pa_status_t pa_bm_add_sequence(pa_block_manager* bm, int64_t seq_id, const int64
         id = bm->allocate();
         if (full && tk) bm->register_full(id, parent, tk, block_hash(parent, tk, bs));
       }
-      if (full && tk) parent = block_hash(parent, tk, bs);
+      if (full && tk) {
+        parent = block_hash(parent, tk, bs);
+        s.hashes.push_back(parent);
+      }
       s.blocks.push_back(id);
     }
     s.len = num_tokens;
-    s.tokens_known = token_ids != nullptr;
-    s.last_full_hash = parent;
+    s.known = token_ids ? num_tokens : 0;
     if (token_ids && num_tokens % bs) {
       const int32_t start = (num_tokens / bs) * bs;
       s.tail_tokens.assign(token_ids + start, token_ids + num_tokens);
@@ -262,20 +286,43 @@ pa_status_t pa_bm_append_slots(pa_block_manager* bm, const int64_t* seq_ids, con
     }
     slots_out[i] = (int64_t)s.blocks[pos / bs] * bs + pos % bs;
     s.len = pos + 1;
-    // Prefix cache: a block the step fills, with every token known, is registered.
-    if (token_ids && s.tokens_known) {
-      s.tail_tokens.push_back(token_ids[i]);
-      if (s.len % bs == 0) {
-        const uint64_t h = block_hash(s.last_full_hash, s.tail_tokens.data(), bs);
-        bm->register_full(s.blocks.back(), s.last_full_hash, s.tail_tokens.data(), h);
-        s.last_full_hash = h;
-        s.tail_tokens.clear();
-      }
-    } else {
-      s.tokens_known = false;
-    }
+    if (token_ids && s.known == pos) bm->learn(s, token_ids[i]);
   }
   *num_cow = ncow;
+  return PA_OK;
+}
+
+pa_status_t pa_bm_truncate(pa_block_manager* bm, int64_t seq_id, int32_t new_len, const int64_t* token_ids,
+                           int32_t num_token_ids) {
+  if (!bm || new_len < 0 || num_token_ids < 0 || (num_token_ids > 0 && !token_ids)) return PA_ERR_INVALID;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end() || new_len > it->second.len) return PA_ERR_INVALID;
+  Seq& s = it->second;
+  const int32_t bs = bm->block_size;
+  // The ids name the last kept positions, which were appended without.
+  const int32_t keep_known = s.known < new_len ? s.known : new_len;
+  if (num_token_ids > new_len - keep_known) return PA_ERR_INVALID;
+  const int32_t keep_full = keep_known / bs;
+  const int32_t keep_blocks = (new_len + bs - 1) / bs;
+  while ((int32_t)s.blocks.size() > keep_blocks) {
+    bm->release(s.blocks.back());
+    s.blocks.pop_back();
+  }
+  // Rows of a last block that is cut will be written again, by this sequence
+  // or by a holder that remains: it is no prefix to find any more.
+  if (new_len % bs != 0) bm->unregister(s.blocks.back());
+  if (keep_full == (int32_t)s.hashes.size()) {
+    s.tail_tokens.resize(keep_known - keep_full * bs);
+    s.known = keep_known;
+  } else {  // cut inside or behind an earlier full block, whose ids are not kept: known up to its start
+    s.hashes.resize(keep_full);
+    s.tail_tokens.clear();
+    s.known = keep_full * bs;
+  }
+  s.len = new_len;
+  if (s.known == new_len - num_token_ids) {  // every position before them is known
+    for (int32_t i = 0; i < num_token_ids; ++i) bm->learn(s, token_ids[i]);
+  }
   return PA_OK;
 }
 

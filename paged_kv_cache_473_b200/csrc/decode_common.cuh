@@ -11,8 +11,8 @@
 
 namespace pa {
 
-// Device error word (OR of PA_DEVERR_* bits), one per device.
-__device__ unsigned int g_device_errors;
+// Device error word (OR of PA_DEVERR_* bits), one per device and translation unit.
+static __device__ unsigned int g_device_errors;
 
 __device__ __forceinline__ void raise_error(unsigned int bit) { atomicOr(&g_device_errors, bit); }
 
