@@ -6,6 +6,7 @@
 #include "../../include/pagedattn.h"
 #include "commit_tree.cuh"
 #include "decode_common.cuh"
+#include "decode_tree.cuh"
 #include "decode_tree_common.cuh"
 #include "decode_tree_simt.cuh"
 #include "host_common.cuh"
@@ -88,15 +89,66 @@ cudaError_t launch_tree_simt_t(const TreeParams& p, cudaStream_t st) {
   return launch_ex(pa::decode_tree_simt_kernel<T, D>, grid, dim3(NW * 32), NW * RT * D * 4, st, true, p);
 }
 
-template <typename T>
 cudaError_t launch_tree_simt(const TreeParams& p, int head_dim, cudaStream_t st) {
   switch (head_dim) {
     case 64:
-      return launch_tree_simt_t<T, 64>(p, st);
+      return launch_tree_simt_t<float, 64>(p, st);
     case 128:
-      return launch_tree_simt_t<T, 128>(p, st);
+      return launch_tree_simt_t<float, 128>(p, st);
     default:
-      return launch_tree_simt_t<T, 256>(p, st);
+      return launch_tree_simt_t<float, 256>(p, st);
+  }
+}
+
+// CTAs of the tensor-core kernel: all that are resident at once, a whole number
+// of groups of m_tiles.
+int tree_grid(int head_dim, int m_tiles) {
+  const int resident = sm_count() * (head_dim <= 128 ? pa::TreeCfg<128>::kMinBlocks : pa::TreeCfg<256>::kMinBlocks);
+  return std::max(1, resident / m_tiles) * m_tiles;
+}
+
+int tree_m_tiles(int tree_len, int group) { return (tree_len * group + pa::kTreeRows - 1) / pa::kTreeRows; }
+
+// Workspace of the tensor-core kernel: the counter region of the split-K calls
+// (untouched), one record per CTA, two partials per CTA.
+struct TreeWorkspace {
+  size_t rec, o, ml, bytes;
+};
+TreeWorkspace tree_workspace(int grid, int head_dim, int tree_len, int group) {
+  const size_t rows = std::min(pa::kTreeRows, (tree_len * group + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows *
+                                                  pa::kTreeCombineRows);
+  TreeWorkspace w;
+  w.rec = pa::kCounterBytes;
+  w.o = w.rec + align256((size_t)grid * sizeof(int4));
+  w.ml = w.o + align256(2 * (size_t)grid * rows * head_dim * 4);
+  w.bytes = w.ml + align256(2 * (size_t)grid * rows * 2 * 4);
+  return w;
+}
+
+template <int D>
+cudaError_t launch_tree_t(const TreeParams& p, int grid, cudaStream_t st) {
+  using Cfg = pa::TreeCfg<D>;
+  CUtensorMap kmap, vmap;
+  const long long rows = (long long)p.num_blocks * p.hkv * p.block_size;
+  if (!cache_maps(p.k_cache, p.v_cache, D, rows, &kmap, &vmap)) return cudaErrorInvalidValue;
+  auto kern = pa::decode_tree_kernel<D>;
+  static std::atomic<uint64_t> smem_done{0};
+  cudaError_t e = set_smem(kern, Cfg::kSmemBytes, smem_done);
+  if (e != cudaSuccess) return e;
+  e = launch_ex(kern, dim3(grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, kmap, vmap, p);
+  if (e != cudaSuccess) return e;
+  const int chunks = (std::min(pa::kTreeRows, p.tree_len * p.group) + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows;
+  return launch_ex(pa::tree_combine_kernel<D>, dim3(grid, chunks), dim3(2 * D), 0, st, true, p);
+}
+
+cudaError_t launch_tree(const TreeParams& p, int head_dim, int grid, cudaStream_t st) {
+  switch (head_dim) {
+    case 64:
+      return launch_tree_t<64>(p, grid, st);
+    case 128:
+      return launch_tree_t<128>(p, grid, st);
+    default:
+      return launch_tree_t<256>(p, grid, st);
   }
 }
 
@@ -190,9 +242,12 @@ pa_status_t pa_rope_append(const void* q, int64_t q_stride, const void* k, int64
 
 size_t pa_decode_tree_workspace_size(int32_t batch, int32_t tree_len, int32_t num_q_heads, int32_t head_dim,
                                      int32_t max_context_len, int32_t num_kv_heads) {
-  (void)max_context_len;
+  (void)max_context_len;  // the partials are two per CTA, however long the contexts are
   if (batch <= 0 || tree_len <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_kv_heads <= 0) return 0;
-  return 0;
+  if (tree_len > pa::kMaxTreeNodes || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup)
+    return 0;
+  const int group = num_q_heads / num_kv_heads;
+  return tree_workspace(tree_grid(head_dim, tree_m_tiles(tree_len, group)), head_dim, tree_len, group).bytes;
 }
 
 pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -210,8 +265,15 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   if (tree_len <= 0 || max_context_len <= 0) return PA_ERR_INVALID;
   if (tree_len > pa::kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
   if (mask_stride != 0 && mask_stride < tree_len) return PA_ERR_INVALID;
+  const long long longest = std::min<long long>(max_context_len, (long long)max_blocks_per_seq * block_size);
+  const int group = num_q_heads / num_kv_heads, m_tiles = tree_m_tiles(tree_len, group);
+  if ((longest / pa::kTreeTile + 1) * num_kv_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   if (batch == 0) return PA_OK;
   if (!tree_mask || !aligned(tree_mask, 8) || !aligned(tree_lens, 4)) return PA_ERR_INVALID;
+  const bool tensor_cores = dtype == PA_BF16;
+  const int grid = tree_grid(head_dim, m_tiles);
+  const TreeWorkspace w = tree_workspace(grid, head_dim, tree_len, group);
+  if (tensor_cores && (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes)) return PA_ERR_WORKSPACE;
 
   TreeParams p{};
   p.q = q;
@@ -227,23 +289,28 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   p.tree_len = tree_len;
   p.hq = num_q_heads;
   p.hkv = num_kv_heads;
-  p.group = num_q_heads / num_kv_heads;
+  p.group = group;
   p.block_size = block_size;
   p.log2_bs = ilog2(block_size);
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.window = window;
   p.max_context = max_context_len;
-  p.m_tiles = (tree_len * p.group + 127) / 128;
+  p.m_tiles = m_tiles;
   p.scale = scale;
   p.use_softcap = (softcap > 0.f && std::isfinite(softcap)) ? 1 : 0;
   p.softcap = p.use_softcap ? softcap : 0.f;
-  (void)workspace;
-  (void)workspace_bytes;
-  const cudaError_t e = dtype == PA_F32 ? launch_tree_simt<float>(p, head_dim, stream)
-                                        : launch_tree_simt<__nv_bfloat16>(p, head_dim, stream);
-  if (e != cudaSuccess) return PA_ERR_CUDA;
-  pa_host::set_last_launches(1);
+  if (!tensor_cores) {
+    if (launch_tree_simt(p, head_dim, stream) != cudaSuccess) return PA_ERR_CUDA;
+    pa_host::set_last_launches(1);
+    return PA_OK;
+  }
+  char* ws = static_cast<char*>(workspace);
+  p.ws_rec = reinterpret_cast<int4*>(ws + w.rec);
+  p.ws_o = reinterpret_cast<float*>(ws + w.o);
+  p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+  if (launch_tree(p, head_dim, grid, stream) != cudaSuccess) return PA_ERR_CUDA;
+  pa_host::set_last_launches(2);
   return PA_OK;
 }
 

@@ -65,10 +65,22 @@ TREE = ("q k v bt cl tl mask ms B T hq hkv d bs mb nb scale cap win out dt maxL 
     (dict(T=65, ms=65), UNSUPPORTED), (dict(maxL=0), INVALID), (dict(hq=9), INVALID), (dict(hq=32), UNSUPPORTED),
     (dict(d=96), UNSUPPORTED), (dict(bs=8), UNSUPPORTED), (dict(bs=24), UNSUPPORTED), (dict(dt=3), INVALID),
     (dict(cap=float("nan")), INVALID), (dict(B=70000), UNSUPPORTED), (dict(nb=1 << 27), UNSUPPORTED),
-    (dict(B=0, q=None), OK)])
+    (dict(ws=None), WORKSPACE), (dict(ws=A + 8), WORKSPACE), (dict(wsb=1000), WORKSPACE), (dict(B=0, q=None), OK)])
 def test_tree_host_checks(kw, status):
     assert _call("pa_decode_tree", *TREE, kw) == status
     assert pa.last_launch_count() == 0
+
+
+def test_tree_workspace_size():
+    """Two partials per CTA: grows with the tree's rows up to 128 per kv head, not with batch or context."""
+    one = pa.decode_tree_workspace_size(1, 1, 32, 128, 1024, 8)
+    assert 256 * 1024 < one < pa.decode_tree_workspace_size(1, 8, 32, 128, 1024, 8)
+    most = pa.decode_tree_workspace_size(1, 32, 32, 128, 1024, 8)
+    assert pa.decode_tree_workspace_size(500, 64, 32, 128, 1 << 20, 8) <= most < 64 << 20
+    for bad in ((0, 4, 8, 64, 10, 2), (1, 0, 8, 64, 10, 2), (1, 65, 8, 64, 10, 2), (1, 4, 9, 64, 10, 2), (1, 4, 18, 64, 10, 2)):
+        assert pa.decode_tree_workspace_size(*bad) == 0
+    args = dict(TREE[1], wsb=pa.decode_tree_workspace_size(2, 16, 8, 128, 64, 2) - 1)
+    assert _call("pa_decode_tree", TREE[0], args, {}) == WORKSPACE
 
 
 COMMIT = ("k v layers bt cl tl T acc ma al B hkv d bs mb nb new dt stream",
