@@ -2,9 +2,11 @@
 // tensor cores (tcgen05, accumulators in tensor memory).
 //
 // The n * G query rows of a (sequence, kv head) unit -- row r = (node r / G,
-// head r % G) -- are the 128 rows of one UMMA tile (m_tiles tiles where there
-// are more), whatever the tree looks like: the tree is in the masks of the last
-// keys only.  The unit's keys and values stream in 64-token tiles, as in the
+// head r % G) -- are the 128 rows of one UMMA tile (m_tiles tiles of whole
+// nodes where there are more), whatever the tree looks like: the tree is in the
+// masks of the last keys only.  One 3-D TMA box (64 columns, G heads, the
+// tile's nodes) lands them in that order; rows past them, of shared memory that
+// holds something else, give results that nobody reads.  The unit's keys and values stream in 64-token tiles, as in the
 // prefill kernel: S = Q K^T into one of two TMEM buffers, the softmax by one
 // thread per row, P back into the columns S came from, O += P V in TMEM.
 //
@@ -20,10 +22,12 @@
 // So every CTA streams the same number of tiles whatever the lengths, and the
 // workspace does not grow with the batch.
 //
-// Warps 0-3: softmax, one row per thread; they also load Q and write the rows.
-// Warp 4: MMA issue.  Warp 5: TMA loads (16-row boxes, one per lane).  Every
-// wait is bounded; a wait that gives up raises the abort flag, which ends all
-// roles.
+// Warps 0-3: softmax, one row per thread; they also write the rows.  Warp 4:
+// MMA issue, and the load of a piece's Q as soon as the last S of the piece
+// before is done.  Warp 5: TMA loads of K and V (16-row boxes, one per lane).
+// What a role reads of the next piece (lengths, mask words, block ids) it reads
+// one piece ahead.  Every wait is bounded; a wait that gives up raises the abort
+// flag, which ends all roles.
 //
 // Masks.  A tile is masked where it reaches before a row's window, into the
 // tree or past the sequence's end, or where a block id is bad; there each
@@ -48,12 +52,14 @@ constexpr int kTreeMinTiles = 2;   // shortest range of a CTA: below, a piece's 
 constexpr int kTreeThreads = 192;
 constexpr int kTreeCombineRows = 8;
 
-template <int D>
+// QR: rows of Q that shared memory holds (64 or 128).  At head_dim 128 and 256
+// the 64 rows that smaller trees leave free are one more V stage.
+template <int D, int QR>
 struct TreeCfg {
   static constexpr int kPanels = D / 64;  // 64-element (128-byte) column panels
   static constexpr int kKStages = D <= 64 ? 6 : 3;
-  static constexpr int kVStages = D <= 64 ? 6 : 2;
-  static constexpr int kQPanelBytes = kTreeRows * 128;
+  static constexpr int kVStages = D <= 64 ? 6 : (QR <= 64 ? 3 : 2);
+  static constexpr int kQPanelBytes = QR * 128;
   static constexpr int kKVPanelBytes = kTreeTile * 128;
   static constexpr int kKBytes = kPanels * kKVPanelBytes;
   static constexpr int kQOff = 0;
@@ -68,11 +74,11 @@ struct TreeCfg {
 };
 
 // What the CTA's threads share besides the tiles (behind them, at kBarOff).
-template <int D>
+template <int D, int QR>
 struct TreeShared {
-  using C = TreeCfg<D>;
+  using C = TreeCfg<D, QR>;
   uint64_t kfull[C::kKStages], kempty[C::kKStages], vfull[C::kVStages], vempty[C::kVStages];
-  uint64_t sfull[2], pready[2], odone[2], qready, drain;
+  uint64_t sfull[2], pready[2], odone[2], qfull, drain;
   uint64_t bad[3][4];      // by piece: rows of V with elements that are not finite, in each masked tile
   long long scan[8];
   long long w0, w1, per;   // the CTA's range of tiles
@@ -95,9 +101,22 @@ struct TreeWalk {
   long long w, w1;
   int b, off, tiles, ulo;
   TreeSeq s;
+  int next_len, next_nodes;  // of sequence b + 1, loaded ahead
 
-  __device__ __forceinline__ void load(const TreeParams& p) {
-    s = tree_seq(p, b, false);
+  __device__ __forceinline__ void start(const TreeParams& p, long long from, long long to, int b0, int off0) {
+    w = from;
+    w1 = to;
+    b = b0;
+    off = off0;
+    next_len = p.context_lens[b];
+    next_nodes = p.tree_lens ? p.tree_lens[b] : p.tree_len;
+    load(p);
+  }
+  __device__ __forceinline__ void load(const TreeParams& p) {  // sequence b, whose lengths are here
+    s = tree_fit(p, next_len, next_nodes, false);
+    const int after = min(b + 1, p.batch - 1);
+    next_len = p.context_lens[after];
+    next_nodes = p.tree_lens ? p.tree_lens[after] : p.tree_len;
     ulo = tree_start(s, p.window);
     tiles = s.n > 0 ? (s.L - (ulo & ~(kTreeTile - 1)) + kTreeTile - 1) / kTreeTile : 0;
   }
@@ -116,7 +135,7 @@ struct TreeWalk {
       o.start = w;
       w += n;
       off += n;
-      if (mt * kTreeRows >= s.n * p.group) continue;  // this tree has no rows in the CTA's row tile
+      if (mt * p.q_nodes >= s.n) continue;  // this tree has no rows in the CTA's row tile
       o.b = b;
       o.tiles = tiles;
       o.s = s;
@@ -200,15 +219,15 @@ __device__ __forceinline__ void tree_locate(const TreeParams& p, int grp, int gr
 // slot at [d / 4][r][d % 4], so that a warp's rows are neighbours, and (m, l)
 // of a row behind.
 __device__ __forceinline__ int tree_row_stride(const TreeParams& p) {
-  return min(kTreeRows, (p.tree_len * p.group + kTreeCombineRows - 1) & ~(kTreeCombineRows - 1));
+  return (p.q_nodes * p.group + kTreeCombineRows - 1) & ~(kTreeCombineRows - 1);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
-    decode_tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const TreeParams p) {
-  using C = TreeCfg<D>;
-  using Shared = TreeShared<D>;
+template <int D, int QR>
+__global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
+    decode_tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
+  using C = TreeCfg<D, QR>;
+  using Shared = TreeShared<D, QR>;
   static_assert(sizeof(Shared) <= C::kSmemBytes - C::kBarOff, "shared area");
   constexpr uint32_t FULL = 0xffffffffu;
   constexpr int NK = C::kKStages, NV = C::kVStages, TILE = kTreeTile;
@@ -231,10 +250,11 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
       mbar_init(bar(sh.pready[s]), 4);
       mbar_init(bar(sh.odone[s]), 1);
     }
-    mbar_init(bar(sh.qready), 4);
+    mbar_init(bar(sh.qfull), 1);
     mbar_init(bar(sh.drain), 1);
     sh.abort = 0;
     mbar_init_fence();
+    prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
@@ -256,16 +276,12 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
       }
     }
   }
-  TreeWalk walk;
-  walk.w = sh.w0;
-  walk.w1 = sh.w1;
-  if (walk.w >= walk.w1) {  // the same in all threads
+  if (sh.w0 >= sh.w1) {  // the same in all threads
     if (tid == 0) p.ws_rec[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  walk.b = sh.b0;
-  walk.off = sh.off0;
-  walk.load(p);
+  TreeWalk walk;
+  walk.start(p, sh.w0, sh.w1, sh.b0, sh.off0);
 
   if (warp == 0) umma::alloc(smem_addr(&sh.tmem), C::kTmemCols);
   umma::fence_before();
@@ -386,13 +402,13 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
       }
     }
   } else if (warp == 4) {
-    // ================= MMA issuer (lane 0) =================
+    // ================= MMA issuer (one elected lane) =================
     const uint32_t idesc_s = umma::idesc_bf16(kTreeRows, TILE, 0, 0);
     const uint32_t idesc_o = umma::idesc_bf16(kTreeRows, D, 0, 1);
     auto s_mma = [&](int n) {  // S(n) = Q K(n)^T into buffer n % 2
       if (!wait_use(sh.kfull[n % NK], n / NK)) return false;
       umma::fence_after();
-      if (lane == 0) {
+      if (umma::elect()) {
         const uint32_t kst = k_s + (n % NK) * C::kKBytes;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -410,7 +426,7 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
       if (!wait_use(sh.pready[n & 1], n >> 1) || *abort_flag) return false;
       if (!wait_use(sh.vfull[n % NV], n / NV)) return false;
       umma::fence_after();
-      if (lane == 0) {
+      if (umma::elect()) {
         const uint32_t vst = v_s + (n % NV) * C::kKBytes;
         const uint32_t pcol = tmem + C::kSCol + (n & 1) * TILE;
 #pragma unroll
@@ -424,15 +440,30 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
       __syncwarp();
       return true;
     };
+    int q_issued = 0;  // Q loads issued, in the lane that issues them
     // S of a tile goes out before P V of the tile before, except where a piece
-    // starts: its Q is loaded only after the last piece's last S.
+    // starts: its Q takes the place of the last piece's, so its first S waits
+    // for that load, and P V of the tile before does not wait for it.
     bool ok = true, before_first = false;
     int n = 0;
-    TreePiece c;
-    for (int u = 0; ok && walk.next(p, mt, c); ++u) {
+    TreePiece c, nxt;
+    bool more = walk.next(p, mt, nxt);
+    for (int u = 0; ok && more; ++u) {
+      c = nxt;
       for (int i = c.t0; ok && i < c.t1; ++i, ++n) {
         if (i == c.t0) {
-          ok = (n == 0 || o_mma(n - 1, before_first)) && wait_use(sh.qready, u) && s_mma(n);
+          ok = n == 0 || wait_use(sh.sfull[(n - 1) & 1], (n - 1) >> 1);
+          if (!ok) break;
+          if (umma::elect()) {
+            mbar_arrive_expect_tx(bar(sh.qfull), C::kPanels * p.q_nodes * G * 128);
+            for (int k = 0; k < C::kPanels; ++k)
+              tma_load_3d(q_s + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k * 64, c.g * G,
+                          c.b * p.tree_len + mt * p.q_nodes);
+            q_issued = u + 1;
+          }
+          __syncwarp();
+          ok = (n == 0 || o_mma(n - 1, before_first)) && wait_use(sh.qfull, u) && s_mma(n);
+          more = ok && walk.next(p, mt, nxt);
         } else {
           ok = s_mma(n) && o_mma(n - 1, before_first);
         }
@@ -442,7 +473,10 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
     if (ok && n > 0) ok = o_mma(n - 1, before_first);
     if (!ok) give_up();
     if (!ok || *abort_flag) {  // the MMAs issued get a bounded time to finish before TMEM is freed
-      if (lane == 0) umma::commit(bar(sh.drain));
+      if (umma::elect()) {
+        umma::commit(bar(sh.drain));
+        if (q_issued > 0) (void)mbar_wait_bounded(bar(sh.qfull), (q_issued - 1) & 1, kDrainLimitNs);
+      }
       (void)mbar_wait_bounded(bar(sh.drain), 0, kDrainLimitNs);
     }
   } else {
@@ -458,44 +492,20 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
     const float cap_a = p.softcap * kLog2e, cap_b = 2.f * cap_a;
     const float cap_c = p.use_softcap ? 2.f * xs_all / p.softcap : 0.f;
 
-    // Q of a piece into shared memory (canonical K-major SWIZZLE_128B); rows past the tree are zero.
-    auto load_q = [&](const TreePiece& c) {
-      const int rows = c.s.n * G - mt * kTreeRows;
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        const int idx = i * 128 + tid, qr = idx / (D / 8), ch = idx % (D / 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (qr < rows) {
-          const int gr = mt * kTreeRows + qr;
-          x = *reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(p.q) +
-              (((int64_t)c.b * p.tree_len + gr / G) * p.hq + (int64_t)c.g * G + gr % G) * D + ch * 8);
-        }
-        const uint32_t dst = q_s + (ch >> 3) * C::kQPanelBytes + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                     : "memory");
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh.qready));
-    };
-
     TreePiece c, nxt;
+    TreeRow row, row_nxt;
+    const int node = mt * p.q_nodes + r / G;  // this thread's row: its node and its head
+    const int64_t head = (int64_t)node * p.hq + r % G;
     bool ok = true, more = walk.next(p, mt, nxt);
+    if (more) row_nxt = tree_row(p, nxt.s, nxt.b, node);
     int4 rec = make_int4(0, 0, 0, 0);
-    if (more) load_q(nxt);
     int n = 0;
     for (int u = 0; ok && more; ++u) {
       c = nxt;
-      more = walk.next(p, mt, nxt);
-      const int rows = min(kTreeRows, c.s.n * G - mt * kTreeRows);
+      row = row_nxt;
+      const int rows = min(p.q_nodes, c.s.n - mt * p.q_nodes) * G;
       const bool real = r < rows, active = 32 * warp < rows;
-      const int gr = mt * kTreeRows + r;
       const int L = c.s.L, base = c.s.base;
-      TreeRow row;
-      row.lo = base;
-      row.nodes = 0;
-      if (real) row = tree_row(p, c.s, c.b, gr / G);
       // Rows' windows start in [ulo, ulo + 63] (a depth is at most 63) and at most at base.
       const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;
       uint64_t* bad = sh.bad[u % 3];
@@ -577,7 +587,8 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
           l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
           umma::st16_nowait(s_col, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
           umma::st16_nowait(s_col + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
-          if (i > c.t0 && __any_sync(FULL, moved)) {  // the first tile's P V overwrites O
+          // (The first tile's P V overwrites O; rows that nobody reads move nothing.)
+          if (i > c.t0 && __any_sync(FULL, moved && real)) {
             ok = wait_use(sh.odone[(n - 1) & 1], (n - 1) >> 1);
             if (!ok) break;
             umma::fence_after();
@@ -596,26 +607,50 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
           ok = wait_use(sh.vfull[n % NV], n / NV);
           if (!ok) break;
           const uint32_t vst = v_s + (n % NV) * C::kKBytes;
-          const int slot = kt + TILE > base ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - c.kt0) / TILE;
-          for (int idx = tid; idx < TILE * C::kPanels * 8; idx += 128) {
-            const int k = idx / (C::kPanels * 8), rem = idx % (C::kPanels * 8);
-            const uint32_t dst = vst + (rem >> 3) * C::kKVPanelBytes + k * 128 + ((rem & 7) << 4);
-            const int t = kt + k;
-            if (t < c.ulo || t >= L || ((skip >> (k >> 4)) & 1u)) {
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u) : "memory");
-            } else if (edge) {
-              uint32_t w[4], bits = 0;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(dst));
+          constexpr int CPR = C::kPanels * 8;  // 16-byte chunks of a row
+          auto chunk = [&](int idx) {          // row idx / CPR; where a row's chunks are does not matter
+            const int k = idx / CPR, rem = idx % CPR;
+            return vst + (rem >> 3) * C::kKVPanelBytes + k * 128 + ((rem & 7) << 4);
+          };
+          // Rows of V that no row attends: zero (they were not loaded, or hold what stands behind the end).
+          uint64_t none = low_bits(min(max(c.ulo - kt, 0), TILE)) | ~low_bits(min(max(L - kt, 0), TILE));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {  // exponent bits all set: not finite
-                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, bits = 1;
-                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, bits = 1;
-              }
-              if (bits) {
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                             "r"(w[3])
+          for (int k = 0; k < 4; ++k)
+            if ((skip >> k) & 1u) none |= 0xffffull << (16 * k);
+          if (none) {
+            for (int idx = tid; idx < TILE * CPR; idx += 128)
+              if ((none >> (idx / CPR)) & 1ull)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(idx)), "r"(0u) : "memory");
+          }
+          if (edge) {
+            const int slot = kt + TILE > base ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - c.kt0) / TILE;
+            constexpr int U = 4;
+#pragma unroll 1
+            for (int i0 = tid; i0 < TILE * CPR; i0 += 128 * U) {
+              uint32_t w[U][4], top = 0;
+#pragma unroll
+              for (int e = 0; e < U; ++e)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                             : "r"(chunk(i0 + 128 * e)));
+#pragma unroll
+              for (int e = 0; e < U; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[e][j] & 0x7f807f80u);
+              // Exponent bits all set in some element: not finite.  (Rows just
+              // zeroed by another thread may still read as what stood there.)
+              if ((top & 0xffffu) != 0x7f80u && (top >> 16) != 0x7f80u) continue;
+              for (int e = 0; e < U; ++e) {
+                const int idx = i0 + 128 * e, k = idx / CPR;
+                if ((none >> k) & 1ull) continue;
+                bool found = false;
+                for (int j = 0; j < 4; ++j) {
+                  if ((w[e][j] & 0x7f80u) == 0x7f80u) w[e][j] &= 0xffff0000u, found = true;
+                  if ((w[e][j] & 0x7f800000u) == 0x7f800000u) w[e][j] &= 0xffffu, found = true;
+                }
+                if (!found) continue;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(idx)), "r"(w[e][0]),
+                             "r"(w[e][1]), "r"(w[e][2]), "r"(w[e][3])
                              : "memory");
                 atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << k);
               }
@@ -629,10 +664,12 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
         umma::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.pready[n & 1]));
+        if (i == c.t0) {  // the next piece, while the tensor core is at this one
+          more = walk.next(p, mt, nxt);
+          if (more) row_nxt = tree_row(p, nxt.s, nxt.b, node);
+        }
       }
       if (!ok || *abort_flag) break;
-      // The piece's last S is done: its Q may go.
-      if (more) load_q(nxt);
 
       // ---- write the piece's rows -------------------------------------------------------
       const bool begins = c.t0 == 0, ends = c.t1 == c.tiles;
@@ -647,9 +684,9 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D>::kMinBlocks)
       const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
       float* po = p.ws_o + (int64_t)slot * row_stride * D + r * 4;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
-                            (((int64_t)c.b * p.tree_len + gr / G) * p.hq + (int64_t)c.g * G + gr % G) * D;
+                            ((int64_t)c.b * p.tree_len * p.hq + (int64_t)c.g * G + head) * D;
       if (active) {
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < D / 16; ++k) {
           float v[16];
           umma::ld16(lane_base + C::kOCol + k * 16, v);
@@ -723,7 +760,7 @@ __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p)
   const int r = blockIdx.y * kTreeCombineRows + (threadIdx.x & (kTreeCombineRows - 1));
   const int col4 = threadIdx.x / kTreeCombineRows;
   if (rec.x == 0 || r >= rec.w) return;
-  const int row_stride = tree_row_stride(p), mt = c % p.m_tiles, gr = mt * kTreeRows + r;
+  const int row_stride = tree_row_stride(p), G = p.group, node = c % p.m_tiles * p.q_nodes + r / G;
   auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k * p.m_tiles)); };
   float M = -CUDART_INF_F;
   for (int k = 0; k < rec.x; ++k) M = fmaxf(M, p.ws_ml[(slot(k) * row_stride + r) * 2]);
@@ -742,9 +779,8 @@ __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p)
     acc.w = fmaf(w, o.w, acc.w);
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;  // a row that attends nothing is zero
-  const int G = p.group;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                       (((int64_t)rec.y * p.tree_len + gr / G) * p.hq + (int64_t)rec.z * G + gr % G) * D + col4 * 4;
+                       (((int64_t)rec.y * p.tree_len + node) * p.hq + (int64_t)rec.z * G + r % G) * D + col4 * 4;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 

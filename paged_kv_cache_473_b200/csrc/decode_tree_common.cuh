@@ -33,7 +33,7 @@ struct TreeParams {
   int batch, tree_len, hq, hkv, group;
   int block_size, log2_bs, max_blocks, num_blocks;
   int window, max_context;
-  int m_tiles;                  // 128-row tiles of tree_len * group query rows
+  int q_nodes, m_tiles;         // nodes per row tile of at most 128 query rows, row tiles of a tree_len tree
   float scale, softcap;
   int use_softcap;
 };
@@ -45,10 +45,10 @@ struct TreeSeq {
   int L, n, base;
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b, bool report) {
+__device__ __forceinline__ TreeSeq tree_fit(const TreeParams& p, int len, int nodes, bool report) {
   TreeSeq s;
-  s.L = p.context_lens[b];
-  s.n = p.tree_lens ? p.tree_lens[b] : p.tree_len;
+  s.L = len;
+  s.n = nodes;
   const int cap = min(p.max_context, p.max_blocks << p.log2_bs);
   if (s.L != 0 && (s.L < 0 || s.L > cap || s.n < 0 || s.n > p.tree_len || s.L < s.n)) {
     if (report) raise_error(PA_DEVERR_CONTEXT);
@@ -57,6 +57,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b, bool rep
   if (s.L == 0) s.n = 0;
   s.base = s.L - s.n;
   return s;
+}
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b, bool report) {
+  return tree_fit(p, p.context_lens[b], p.tree_lens ? p.tree_lens[b] : p.tree_len, report);
 }
 
 // First position that any node of the tree may attend (the root's window start).

@@ -100,55 +100,67 @@ cudaError_t launch_tree_simt(const TreeParams& p, int head_dim, cudaStream_t st)
   }
 }
 
-// CTAs of the tensor-core kernel: all that are resident at once, a whole number
-// of groups of m_tiles.
-int tree_grid(int head_dim, int m_tiles) {
-  const int resident = sm_count() * (head_dim <= 128 ? pa::TreeCfg<128>::kMinBlocks : pa::TreeCfg<256>::kMinBlocks);
-  return std::max(1, resident / m_tiles) * m_tiles;
-}
-
-int tree_m_tiles(int tree_len, int group) { return (tree_len * group + pa::kTreeRows - 1) / pa::kTreeRows; }
-
-// Workspace of the tensor-core kernel: the counter region of the split-K calls
-// (untouched), one record per CTA, two partials per CTA.
-struct TreeWorkspace {
+// How the tensor-core kernel takes a call.  A row tile is a whole number of
+// nodes; the grid is all CTAs that are resident at once, a whole number of
+// groups of m_tiles.  Workspace: the counter region of the split-K calls
+// (untouched), one record per CTA, two partials of `rows` rows per CTA.
+struct TreePlan {
+  int q_nodes, m_tiles, grid, rows;
   size_t rec, o, ml, bytes;
 };
-TreeWorkspace tree_workspace(int grid, int head_dim, int tree_len, int group) {
-  const size_t rows = std::min(pa::kTreeRows, (tree_len * group + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows *
-                                                  pa::kTreeCombineRows);
-  TreeWorkspace w;
+TreePlan tree_plan(int head_dim, int tree_len, int group) {
+  TreePlan w;
+  w.q_nodes = std::min(tree_len, pa::kTreeRows / group);
+  w.m_tiles = (tree_len + w.q_nodes - 1) / w.q_nodes;
+  const int per_sm = head_dim <= 128 ? pa::TreeCfg<128, 128>::kMinBlocks : pa::TreeCfg<256, 128>::kMinBlocks;
+  w.grid = std::max(1, sm_count() * per_sm / w.m_tiles) * w.m_tiles;
+  w.rows = (w.q_nodes * group + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows * pa::kTreeCombineRows;
   w.rec = pa::kCounterBytes;
-  w.o = w.rec + align256((size_t)grid * sizeof(int4));
-  w.ml = w.o + align256(2 * (size_t)grid * rows * head_dim * 4);
-  w.bytes = w.ml + align256(2 * (size_t)grid * rows * 2 * 4);
+  w.o = w.rec + align256((size_t)w.grid * sizeof(int4));
+  w.ml = w.o + align256(2 * (size_t)w.grid * w.rows * head_dim * 4);
+  w.bytes = w.ml + align256(2 * (size_t)w.grid * w.rows * 2 * 4);
   return w;
 }
 
-template <int D>
-cudaError_t launch_tree_t(const TreeParams& p, int grid, cudaStream_t st) {
-  using Cfg = pa::TreeCfg<D>;
-  CUtensorMap kmap, vmap;
+// q as a 3-D tensor [batch * tree_len][num_q_heads][head_dim]; a box is 64
+// columns (128 B) x one kv head's heads x the nodes of a row tile.
+bool encode_q_map(CUtensorMap* map, const TreeParams& p, int head_dim) {
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)p.hq, (cuuint64_t)p.batch * p.tree_len};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)p.hq * head_dim * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)p.q_nodes};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int QR>
+cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t st) {
+  using Cfg = pa::TreeCfg<D, QR>;
+  CUtensorMap qmap, kmap, vmap;
   const long long rows = (long long)p.num_blocks * p.hkv * p.block_size;
-  if (!cache_maps(p.k_cache, p.v_cache, D, rows, &kmap, &vmap)) return cudaErrorInvalidValue;
-  auto kern = pa::decode_tree_kernel<D>;
+  if (!tensor_map_encoder() || !encode_q_map(&qmap, p, D) || !encode_cache_map(&kmap, p.k_cache, D, rows) ||
+      !encode_cache_map(&vmap, p.v_cache, D, rows))
+    return cudaErrorInvalidValue;
+  auto kern = pa::decode_tree_kernel<D, QR>;
   static std::atomic<uint64_t> smem_done{0};
   cudaError_t e = set_smem(kern, Cfg::kSmemBytes, smem_done);
   if (e != cudaSuccess) return e;
-  e = launch_ex(kern, dim3(grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, kmap, vmap, p);
+  e = launch_ex(kern, dim3(w.grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  const int chunks = (std::min(pa::kTreeRows, p.tree_len * p.group) + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows;
-  return launch_ex(pa::tree_combine_kernel<D>, dim3(grid, chunks), dim3(2 * D), 0, st, true, p);
+  return launch_ex(pa::tree_combine_kernel<D>, dim3(w.grid, w.rows / pa::kTreeCombineRows), dim3(2 * D), 0, st, true,
+                   p);
 }
 
-cudaError_t launch_tree(const TreeParams& p, int head_dim, int grid, cudaStream_t st) {
+cudaError_t launch_tree(const TreeParams& p, int head_dim, const TreePlan& w, cudaStream_t st) {
+  const bool small = w.rows <= 64;
   switch (head_dim) {
     case 64:
-      return launch_tree_t<64>(p, grid, st);
+      return launch_tree_t<64, 128>(p, w, st);
     case 128:
-      return launch_tree_t<128>(p, grid, st);
+      return small ? launch_tree_t<128, 64>(p, w, st) : launch_tree_t<128, 128>(p, w, st);
     default:
-      return launch_tree_t<256>(p, grid, st);
+      return small ? launch_tree_t<256, 64>(p, w, st) : launch_tree_t<256, 128>(p, w, st);
   }
 }
 
@@ -246,8 +258,7 @@ size_t pa_decode_tree_workspace_size(int32_t batch, int32_t tree_len, int32_t nu
   if (batch <= 0 || tree_len <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_kv_heads <= 0) return 0;
   if (tree_len > pa::kMaxTreeNodes || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup)
     return 0;
-  const int group = num_q_heads / num_kv_heads;
-  return tree_workspace(tree_grid(head_dim, tree_m_tiles(tree_len, group)), head_dim, tree_len, group).bytes;
+  return tree_plan(head_dim, tree_len, num_q_heads / num_kv_heads).bytes;
 }
 
 pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -266,13 +277,11 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   if (tree_len > pa::kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
   if (mask_stride != 0 && mask_stride < tree_len) return PA_ERR_INVALID;
   const long long longest = std::min<long long>(max_context_len, (long long)max_blocks_per_seq * block_size);
-  const int group = num_q_heads / num_kv_heads, m_tiles = tree_m_tiles(tree_len, group);
   if ((longest / pa::kTreeTile + 1) * num_kv_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   if (batch == 0) return PA_OK;
   if (!tree_mask || !aligned(tree_mask, 8) || !aligned(tree_lens, 4)) return PA_ERR_INVALID;
   const bool tensor_cores = dtype == PA_BF16;
-  const int grid = tree_grid(head_dim, m_tiles);
-  const TreeWorkspace w = tree_workspace(grid, head_dim, tree_len, group);
+  const TreePlan w = tree_plan(head_dim, tree_len, num_q_heads / num_kv_heads);
   if (tensor_cores && (!workspace || !aligned(workspace, 16) || workspace_bytes < w.bytes)) return PA_ERR_WORKSPACE;
 
   TreeParams p{};
@@ -289,14 +298,15 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   p.tree_len = tree_len;
   p.hq = num_q_heads;
   p.hkv = num_kv_heads;
-  p.group = group;
+  p.group = num_q_heads / num_kv_heads;
   p.block_size = block_size;
   p.log2_bs = ilog2(block_size);
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.window = window;
   p.max_context = max_context_len;
-  p.m_tiles = m_tiles;
+  p.q_nodes = w.q_nodes;
+  p.m_tiles = w.m_tiles;
   p.scale = scale;
   p.use_softcap = (softcap > 0.f && std::isfinite(softcap)) ? 1 : 0;
   p.softcap = p.use_softcap ? softcap : 0.f;
@@ -309,7 +319,7 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   p.ws_rec = reinterpret_cast<int4*>(ws + w.rec);
   p.ws_o = reinterpret_cast<float*>(ws + w.o);
   p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
-  if (launch_tree(p, head_dim, grid, stream) != cudaSuccess) return PA_ERR_CUDA;
+  if (launch_tree(p, head_dim, w, stream) != cudaSuccess) return PA_ERR_CUDA;
   pa_host::set_last_launches(2);
   return PA_OK;
 }

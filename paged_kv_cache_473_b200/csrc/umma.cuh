@@ -52,6 +52,15 @@ __device__ __forceinline__ void commit(uint32_t mbar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of the (converged) warp, always the same: the one that issues MMAs
+// and commits.  Behind this predicate the compiler knows that one thread is
+// active and feeds the instructions' uniform operands directly.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(one));
+  return one != 0;
+}
+
 // Whole warp: allocate ncols TMEM columns; the address lands in shared memory at dst.
 __device__ __forceinline__ void alloc(uint32_t dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
