@@ -6,28 +6,36 @@
 // nodes where there are more), whatever the tree looks like: the tree is in the
 // masks of the last keys only.  One 3-D TMA box (64 columns, G heads, the
 // tile's nodes) lands them in that order; rows past them, of shared memory that
-// holds something else, give results that nobody reads.  The unit's keys and values stream in 64-token tiles, as in the
-// prefill kernel: S = Q K^T into one of two TMEM buffers, the softmax by one
+// holds something else, give results that nobody reads.  The unit's keys and
+// values stream in 64-token tiles: S = Q K^T into TMEM, the softmax by one
 // thread per row, P back into the columns S came from, O += P V in TMEM.
 //
-// Split.  The tiles of all units, in order, are one line of work that is cut
-// into equal ranges, one for each group of m_tiles CTAs (as many CTAs as are
-// resident at once; the CTAs of a group take the same keys for another 128 rows
-// at about the same time, so that these are read from DRAM once).  A CTA runs
-// the pieces of units in its range one after the other; its loads run on into
-// the next piece while the softmax is still at the last one.  A unit that lies
-// in one range is written as rows of `out`; the pieces of one that is cut are
-// written as partials, at most two per CTA (the piece that comes from the range
-// before, the one that goes on in the next), and joined by tree_combine_kernel.
-// So every CTA streams the same number of tiles whatever the lengths, and the
-// workspace does not grow with the batch.
+// One CTA per SM, two groups of softmax warps.
+//   Not PAIR (one row tile): the groups take the tiles in turn.  They share O and
+//     the running maximum, which is handed from tile to tile through shared
+//     memory as soon as a tile's maximum is known, so that a group's exponentials
+//     run beside the other's; each group sums its own weights.
+//   PAIR (two row tiles, head_dim 64 and 128): each group has a row tile and an O
+//     of its own, and both use every tile, so K and V come to the SM once for 256
+//     rows.  (Two CTAs with a row tile each, as before, read them twice and were
+//     bound by that: 8 trees of 64 over 16K-128K keys 583 us, every byte
+//     twice from DRAM.)
 //
-// Warps 0-3: softmax, one row per thread; they also write the rows.  Warp 4:
-// MMA issue, and the load of a piece's Q as soon as the last S of the piece
-// before is done.  Warp 5: TMA loads of K and V (16-row boxes, one per lane).
-// What a role reads of the next piece (lengths, mask words, block ids) it reads
-// one piece ahead.  Every wait is bounded; a wait that gives up raises the abort
-// flag, which ends all roles.
+// Split.  The tiles of all units, in order, are one line of work.  Its first
+// part is cut into one range for each CTA (of a row tile or pair); the rest into
+// shorter ranges that CTAs claim when they are done, since SMs stream at rates up
+// to a third apart.  A range is a sequence of pieces of units; loads run on into the
+// next piece while the softmax is still at the last one.  A unit that lies in one
+// range is written as rows of `out`; the pieces of one that is cut are written as
+// partials, at most two per range (the piece that comes from the range before,
+// the one that goes on in the next), and joined by tree_combine_kernel.  Which CTA
+// takes a range changes no bit of the result.
+//
+// Warps 0-7: softmax, one row per thread; they also write the rows.  Warp 8: MMA
+// issue, and the load of a piece's Q as soon as the last S of the piece before
+// is done.  Warp 9: the schedule (pieces go to the other warps through a ring in
+// shared memory) and the TMA loads of K and V (16-row boxes, one per lane).  Every wait
+// is bounded; a wait that gives up raises the abort flag, which ends all roles.
 //
 // Masks.  A tile is masked where it reaches before a row's window, into the
 // tree or past the sequence's end, or where a block id is bad; there each
@@ -46,195 +54,225 @@
 
 namespace pa {
 
-constexpr int kTreeRows = 128;     // query rows per CTA (UMMA M)
-constexpr int kTreeTile = 64;      // keys per tile
-constexpr int kTreeMinTiles = 2;   // shortest range of a CTA: below, a piece's fixed cost outweighs its tiles
-constexpr int kTreeThreads = 192;
+constexpr int kTreeRows = 128;  // query rows per row tile (UMMA M)
+constexpr int kTreeTile = 64;   // keys per tile
+constexpr int kTreeWarps = 10;
+constexpr int kTreeThreads = kTreeWarps * 32;
 constexpr int kTreeCombineRows = 8;
+constexpr int kTreeMinTiles = 2;    // shortest range: below, a piece's fixed cost outweighs its tiles
+// Claimed ranges: the last 3/16 of the line in up to two per CTA, where a CTA's
+// share is at least kTreeClaimTiles tiles (a shorter share is all one range).
+constexpr int kTreeClaimTiles = 48;
+constexpr int kTreeClaimsPerCta = 2;
+constexpr int kTreeMaxPairs = 4;    // 512 rows in row tiles of one: counters in use
+constexpr int kTreePieces = 4;      // ring of pieces between the roles
 
-// QR: rows of Q that shared memory holds (64 or 128).  At head_dim 128 and 256
-// the 64 rows that smaller trees leave free are one more V stage.
-template <int D, int QR>
+// QR: rows of Q that shared memory holds (64 or 128).
+template <int D, int QR, bool PAIR>
 struct TreeCfg {
   static constexpr int kPanels = D / 64;  // 64-element (128-byte) column panels
-  static constexpr int kKStages = D <= 64 ? 6 : 3;
-  static constexpr int kVStages = D <= 64 ? 6 : (QR <= 64 ? 3 : 2);
+  static constexpr int kRowTiles = PAIR ? 2 : 1;
   static constexpr int kQPanelBytes = QR * 128;
+  static constexpr int kQBytes = kPanels * kQPanelBytes;  // one row tile
   static constexpr int kKVPanelBytes = kTreeTile * 128;
   static constexpr int kKBytes = kPanels * kKVPanelBytes;
+  static constexpr int kMaxSmem = 232448;
+  static constexpr int kSharedBytes = D <= 128 ? 4096 : 3072;
+  static constexpr int kFit = (kMaxSmem - kSharedBytes - kRowTiles * kQBytes) / kKBytes;
+  static constexpr int kKStages = (kFit + 1) / 2 < 10 ? (kFit + 1) / 2 : 10;
+  static constexpr int kVStages = kFit / 2 < 10 ? kFit / 2 : 10;
   static constexpr int kQOff = 0;
-  static constexpr int kKOff = kPanels * kQPanelBytes;
+  static constexpr int kKOff = kRowTiles * kQBytes;
   static constexpr int kVOff = kKOff + kKStages * kKBytes;
   static constexpr int kBarOff = kVOff + kVStages * kKBytes;
-  static constexpr int kSmemBytes = kBarOff + 768;
-  static constexpr int kSCol = 0;              // two S buffers
-  static constexpr int kOCol = 2 * kTreeTile;  // O: D columns
-  static constexpr int kTmemCols = (2 * kTreeTile + D) <= 256 ? 256 : 512;
-  static constexpr int kMinBlocks = D <= 128 ? 2 : 1;  // resident CTAs per SM: TMEM columns and shared memory allow these
+  static constexpr int kSmemBytes = kBarOff + kSharedBytes;
+  static constexpr int kRing = kKStages <= 4 ? 8 : 16;  // tiles whose rows are remembered: those loaded and not done
+  static constexpr int kLag = PAIR ? 1 : 2;             // tiles that S runs ahead of P V
+  static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
+  static constexpr int kSCol = 256;                     // four S buffers, two per group
+  static_assert(!PAIR || D <= 128, "tensor memory");
+  static_assert(kKStages + kLag + 1 < kRing, "ring");
+};
+
+// A piece: tiles [t0, t1) of the `tiles` tiles of unit (b, g).  b < 0: no more.
+struct TreePiece {
+  int b, g, t0, t1, tiles;
+  int L, n, ulo;  // the sequence's lengths, first attended position
+  int range;
 };
 
 // What the CTA's threads share besides the tiles (behind them, at kBarOff).
-template <int D, int QR>
+template <int D, int QR, bool PAIR>
 struct TreeShared {
-  using C = TreeCfg<D, QR>;
+  using C = TreeCfg<D, QR, PAIR>;
   uint64_t kfull[C::kKStages], kempty[C::kKStages], vfull[C::kVStages], vempty[C::kVStages];
-  uint64_t sfull[2], pready[2], odone[2], qfull, drain;
-  uint64_t bad[3][4];      // by piece: rows of V with elements that are not finite, in each masked tile
-  long long scan[8];
-  long long w0, w1, per;   // the CTA's range of tiles
-  int b0, off0;            // where it starts: sequence, tile within the sequence
-  uint32_t skip[16];       // by tile: slices whose block id is bad
+  uint64_t sfull[2][2], pready[2][2], odone[2][2];  // [group][buffer]
+  uint64_t mready[4][2];                            // [warp of the group][tile parity]
+  uint64_t pfull[kTreePieces], pempty[kTreePieces];
+  uint64_t qfull, epi, ofree, drain;
+  uint64_t bad[3][4];  // by piece: rows of V with elements that are not finite, in each masked tile
+  TreePiece pieces[kTreePieces];
+  int rows[C::kRing][4];   // by tile: cache rows of its slices (-1: not loaded)
+  uint8_t skip[C::kRing];  // by tile: slices whose block id is bad
+  float m[PAIR ? 1 : 2][PAIR ? 1 : QR];  // running maximum, by tile parity
+  float l[PAIR ? 1 : 2][PAIR ? 1 : QR];  // the groups' sums at a piece's end
+  long long before[kTreeWarps + 1];      // tiles before each tenth of the batch
   uint32_t tmem;
   int abort;
 };
 
-// A piece: tiles [t0, t1) of the `tiles` tiles of unit (b, g).
-struct TreePiece {
-  int b, g, t0, t1, tiles;
-  TreeSeq s;
-  int ulo, kt0;     // first attended position; its tile's start
-  long long start;  // tile t0 on the line of all work
-};
+// The line of work and its ranges: [0, groups) of `per` tiles, then claimed ones of `chunk`.
+struct TreeLine {
+  long long total, per, chunk, fixed;  // fixed = tiles of the first `groups` ranges
+  int groups, ranges;
 
-// Walks the pieces of a CTA's range.
-struct TreeWalk {
-  long long w, w1;
-  int b, off, tiles, ulo;
-  TreeSeq s;
-  int next_len, next_nodes;  // of sequence b + 1, loaded ahead
-
-  __device__ __forceinline__ void start(const TreeParams& p, long long from, long long to, int b0, int off0) {
-    w = from;
-    w1 = to;
-    b = b0;
-    off = off0;
-    next_len = p.context_lens[b];
-    next_nodes = p.tree_lens ? p.tree_lens[b] : p.tree_len;
-    load(p);
-  }
-  __device__ __forceinline__ void load(const TreeParams& p) {  // sequence b, whose lengths are here
-    s = tree_fit(p, next_len, next_nodes, false);
-    const int after = min(b + 1, p.batch - 1);
-    next_len = p.context_lens[after];
-    next_nodes = p.tree_lens ? p.tree_lens[after] : p.tree_len;
-    ulo = tree_start(s, p.window);
-    tiles = s.n > 0 ? (s.L - (ulo & ~(kTreeTile - 1)) + kTreeTile - 1) / kTreeTile : 0;
-  }
-  __device__ __forceinline__ bool next(const TreeParams& p, int mt, TreePiece& o) {
-    while (w < w1) {
-      while (off >= p.hkv * tiles) {  // w < w1 <= total: a sequence with tiles left exists
-        if (b + 1 >= p.batch) return false;
-        ++b;
-        off = 0;
-        load(p);
-      }
-      o.g = off / tiles;
-      o.t0 = off - o.g * tiles;
-      const int n = (int)min((long long)(tiles - o.t0), w1 - w);
-      o.t1 = o.t0 + n;
-      o.start = w;
-      w += n;
-      off += n;
-      if (mt * p.q_nodes >= s.n) continue;  // this tree has no rows in the CTA's row tile
-      o.b = b;
-      o.tiles = tiles;
-      o.s = s;
-      o.ulo = ulo;
-      o.kt0 = ulo & ~(kTreeTile - 1);
-      return true;
+  __device__ __forceinline__ void cut(long long all, int n) {
+    total = all;
+    groups = n;
+    const long long share = (all + n - 1) / n;
+    if (share < kTreeClaimTiles) {
+      per = max(share, (long long)kTreeMinTiles);
+      chunk = 1;
+      fixed = all;
+      ranges = n;
+    } else {
+      per = share * 13 / 16;
+      fixed = per * n;
+      const long long rest = all - fixed, most = (long long)n * kTreeClaimsPerCta;
+      chunk = max((rest + most - 1) / most, 1ll);
+      ranges = n + (int)((rest + chunk - 1) / chunk);
     }
-    return false;
+  }
+  __device__ __forceinline__ long long start(int r) const {
+    return min(r < groups ? r * per : fixed + (r - groups) * chunk, r < groups ? fixed : total);
+  }
+  __device__ __forceinline__ int range_of(long long x) const {
+    return x < fixed ? (int)(x / per) : groups + (int)((x - fixed) / chunk);
   }
 };
 
-__device__ __forceinline__ long long tree_tiles(const TreeParams& p, int b, bool report) {
-  const TreeSeq s = tree_seq(p, b, report);
-  if (s.n == 0) return 0;
-  return (long long)p.hkv * ((s.L - (tree_start(s, p.window) & ~(kTreeTile - 1)) + kTreeTile - 1) / kTreeTile);
+__device__ __forceinline__ int tree_unit_tiles(const TreeParams& p, const TreeSeq& s) {
+  return s.n > 0 ? (s.L - (tree_start(s, p.window) & ~(kTreeTile - 1)) + kTreeTile - 1) / kTreeTile : 0;
 }
 
-// Exclusive scan over the CTA's threads (two barriers).
-__device__ __forceinline__ long long tree_scan(long long v, long long* scratch, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sequences a lane takes in a scan of the batch by all warps.
+__device__ __forceinline__ int tree_scan_step(const TreeParams& p) {
+  return (p.batch + kTreeThreads - 1) / kTreeThreads;
+}
+
+// Tiles of this lane's sequences in `warp`'s part of the batch, and before them within that part.
+__device__ __forceinline__ long long tree_lane_tiles(const TreeParams& p, int warp, int lane, bool report,
+                                                     long long& before, long long& all) {
+  const int step = tree_scan_step(p), b0 = (warp * 32 + lane) * step;
+  long long v = 0;
+  for (int b = b0; b < min(b0 + step, p.batch); ++b) v += (long long)p.hkv * tree_unit_tiles(p, tree_seq(p, b, report));
   long long incl = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
-  __syncthreads();
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kTreeThreads / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
-  }
-  return before + incl - v;
+  all = __shfl_sync(0xffffffffu, incl, 31);
+  before = incl - v;
+  return v;
 }
 
-// The range of group grp: its tiles [w0, w1) on the line of all work, and the
-// sequence and the tile within it where the range starts.
-template <typename Shared>
-__device__ __forceinline__ void tree_locate(const TreeParams& p, int grp, int groups, Shared& sh) {
-  const int tid = threadIdx.x;
-  const bool report = blockIdx.x == 0;
-  long long v = tid < p.batch ? tree_tiles(p, tid, report) : 0, total, more = 0;
-  long long before = tree_scan(v, sh.scan, total);
-  if (p.batch > kTreeThreads) {
-    for (int b = tid + kTreeThreads; b < p.batch; b += kTreeThreads) more += tree_tiles(p, b, report);
-    long long rest;
-    tree_scan(more, sh.scan, rest);
-    more = total;  // tiles before the next chunk of sequences
-    total += rest;
-  }
-  const long long per = max((total + groups - 1) / groups, (long long)kTreeMinTiles);
-  const long long w0 = min(grp * per, total);
-  if (tid == 0) {
-    sh.w0 = w0;
-    sh.w1 = min(w0 + per, total);
-    sh.per = per;
-  }
-  if (v > 0 && w0 >= before && w0 < before + v) {
-    sh.b0 = tid;
-    sh.off0 = (int)(w0 - before);
-  }
-  for (int c = kTreeThreads; c < p.batch && w0 >= more; c += kTreeThreads) {  // w0 and `more`: the same in all threads
-    long long chunk;
-    v = c + tid < p.batch ? tree_tiles(p, c + tid, false) : 0;
-    before = more + tree_scan(v, sh.scan, chunk);
-    if (v > 0 && w0 >= before && w0 < before + v) {
-      sh.b0 = c + tid;
-      sh.off0 = (int)(w0 - before);
+// Walks the pieces of a range (one warp, the same in all lanes).
+struct TreeWalk {
+  long long w, w1;
+  int b, off, tiles, ulo;
+  TreeSeq s;
+  int next_len, next_nodes;  // of sequence b + 1, loaded ahead
+
+  // Start at tile `from` of the line, to before `to`; before[i]: tiles before warp part i of the batch.
+  __device__ __forceinline__ void start(const TreeParams& p, const long long* before, long long from, long long to,
+                                        int lane) {
+    constexpr uint32_t FULL = 0xffffffffu;
+    w = from;
+    w1 = to;
+    if (w >= w1) return;
+    const int part = __popc(__ballot_sync(FULL, lane > 0 && lane < kTreeWarps && before[lane] <= from));
+    long long ahead, all;
+    const long long v = tree_lane_tiles(p, part, lane, false, ahead, all);
+    ahead += before[part];
+    const int src = __ffs(__ballot_sync(FULL, v > 0 && from >= ahead && from < ahead + v)) - 1;
+    if (src < 0) {  // cannot be: from < to <= total
+      w = w1;
+      return;
     }
-    more += chunk;
+    long long rel = from - __shfl_sync(FULL, ahead, src);
+    b = (part * 32 + src) * tree_scan_step(p);
+    load(p);
+    while (rel >= (long long)p.hkv * tiles && b + 1 < p.batch) {
+      rel -= (long long)p.hkv * tiles;
+      ++b;
+      load_next(p);
+    }
+    off = (int)rel;
   }
-  __syncthreads();
-}
+  __device__ __forceinline__ void fit(const TreeParams& p, int len, int nodes) {
+    s = tree_fit(p, len, nodes, false);
+    const int after = min(b + 1, p.batch - 1);
+    next_len = p.context_lens[after];
+    next_nodes = p.tree_lens ? p.tree_lens[after] : p.tree_len;
+    ulo = tree_start(s, p.window);
+    tiles = tree_unit_tiles(p, s);
+  }
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    fit(p, p.context_lens[b], p.tree_lens ? p.tree_lens[b] : p.tree_len);
+  }
+  __device__ __forceinline__ void load_next(const TreeParams& p) { fit(p, next_len, next_nodes); }
+  // The next piece that has rows from node `first_node` on; `at`: where its unit starts on the line.
+  __device__ __forceinline__ bool next(const TreeParams& p, int first_node, TreePiece& o, long long& at) {
+    while (w < w1) {
+      while (off >= p.hkv * tiles) {  // w < w1 <= total: a sequence with tiles left exists
+        if (b + 1 >= p.batch) return false;
+        ++b;
+        off = 0;
+        load_next(p);
+      }
+      o.g = off / tiles;
+      o.t0 = off - o.g * tiles;
+      const int n = (int)min((long long)(tiles - o.t0), w1 - w);
+      o.t1 = o.t0 + n;
+      at = w - o.t0;
+      w += n;
+      off += n;
+      if (first_node >= s.n) continue;
+      o.b = b;
+      o.tiles = tiles;
+      o.L = s.L;
+      o.n = s.n;
+      o.ulo = ulo;
+      return true;
+    }
+    return false;
+  }
+};
 
-// Partials: slot 2 c of CTA c for the piece that comes from the range before,
-// 2 c + 1 for the one that goes on in the next; element (row r, column d) of a
-// slot at [d / 4][r][d % 4], so that a warp's rows are neighbours, and (m, l)
-// of a row behind.
+// Partials: of range c and row tile t, slot 2 (c m_tiles + t) for the piece that
+// comes from the range before, the next slot for the one that goes on in the
+// next; element (row r, column d) of a slot at [d / 4][r][d % 4], so that a
+// warp's rows are neighbours, and (m, l) of a row behind.
 __device__ __forceinline__ int tree_row_stride(const TreeParams& p) {
   return (p.q_nodes * p.group + kTreeCombineRows - 1) & ~(kTreeCombineRows - 1);
 }
 
-template <int D, int QR>
-__global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
+template <int D, int QR, bool PAIR>
+__global__ void __launch_bounds__(kTreeThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
-  using C = TreeCfg<D, QR>;
-  using Shared = TreeShared<D, QR>;
-  static_assert(sizeof(Shared) <= C::kSmemBytes - C::kBarOff, "shared area");
+  using C = TreeCfg<D, QR, PAIR>;
+  using Shared = TreeShared<D, QR, PAIR>;
+  static_assert(sizeof(Shared) <= C::kSharedBytes, "shared area");
   constexpr uint32_t FULL = 0xffffffffu;
-  constexpr int NK = C::kKStages, NV = C::kVStages, TILE = kTreeTile;
+  constexpr int NK = C::kKStages, NV = C::kVStages, TILE = kTreeTile, LAG = C::kLag;
   extern __shared__ __align__(1024) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int G = p.group, mt = blockIdx.x % p.m_tiles, grp = blockIdx.x / p.m_tiles;
+  const int G = p.group;
+  const int pairs = (p.m_tiles + C::kRowTiles - 1) / C::kRowTiles;  // CTAs that share a range
+  const int pair = blockIdx.x % pairs, grp = blockIdx.x / pairs, mt0 = pair * C::kRowTiles;
 
   pdl_launch_dependents();  // the combine may launch; it waits for this grid to finish
   if (smem_addr(smem) & 1023) {  // the swizzled tiles need 1024-byte alignment
@@ -245,12 +283,20 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
   if (tid == 0) {
     for (int s = 0; s < NK; ++s) mbar_init(bar(sh.kfull[s]), 1), mbar_init(bar(sh.kempty[s]), 1);
     for (int s = 0; s < NV; ++s) mbar_init(bar(sh.vfull[s]), 1), mbar_init(bar(sh.vempty[s]), 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(sh.sfull[s]), 1);
-      mbar_init(bar(sh.pready[s]), 4);
-      mbar_init(bar(sh.odone[s]), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(sh.sfull[s >> 1][s & 1]), 1);
+      mbar_init(bar(sh.pready[s >> 1][s & 1]), 4);
+      mbar_init(bar(sh.odone[s >> 1][s & 1]), 1);
+      mbar_init(bar(sh.mready[s][0]), 1);
+      mbar_init(bar(sh.mready[s][1]), 1);
+    }
+    for (int s = 0; s < kTreePieces; ++s) {
+      mbar_init(bar(sh.pfull[s]), 1);
+      mbar_init(bar(sh.pempty[s]), 9);  // the MMA warp and the softmax warps
     }
     mbar_init(bar(sh.qfull), 1);
+    mbar_init(bar(sh.epi), 8);
+    mbar_init(bar(sh.ofree), 8);
     mbar_init(bar(sh.drain), 1);
     sh.abort = 0;
     mbar_init_fence();
@@ -259,34 +305,23 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
     prefetch_tensormap(&vmap);
   }
   if (tid < 12) sh.bad[tid / 4][tid % 4] = 0;
+  if (warp == 0) umma::alloc(smem_addr(&sh.tmem), 512);
   pdl_wait();  // a programmatic dependent: nothing of global memory was touched before
-  tree_locate(p, grp, gridDim.x / p.m_tiles, sh);
-
-  // ---- rows that no piece writes: those of nodes that a tree does not have ------------------
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    const TreeSeq s = tree_seq(p, b, false);
-    const int done = s.n * G, all = p.tree_len * G;
-    const int per_head = (all - done) * (D / 8);
-    for (int g = 0; g < p.hkv && per_head > 0; ++g) {
-      for (int i = tid; i < per_head; i += kTreeThreads) {
-        const int r = done + i / (D / 8);
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
-                           (((int64_t)b * p.tree_len + r / G) * p.hq + (int64_t)g * G + r % G) * D + i % (D / 8) * 8;
-        *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
-      }
-    }
+  {
+    long long before, all;
+    tree_lane_tiles(p, warp, lane, blockIdx.x == 0, before, all);
+    if (lane == 0) sh.before[warp + 1] = all;
   }
-  if (sh.w0 >= sh.w1) {  // the same in all threads
-    if (tid == 0) p.ws_rec[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  TreeWalk walk;
-  walk.start(p, sh.w0, sh.w1, sh.b0, sh.off0);
-
-  if (warp == 0) umma::alloc(smem_addr(&sh.tmem), C::kTmemCols);
   umma::fence_before();
   __syncthreads();
   umma::fence_after();
+  if (tid == 0) {
+    sh.before[0] = 0;
+    for (int i = 1; i <= kTreeWarps; ++i) sh.before[i] += sh.before[i - 1];
+  }
+  __syncthreads();
+  TreeLine line;
+  line.cut(sh.before[kTreeWarps], gridDim.x / pairs);
   const uint32_t tmem = sh.tmem;
   const uint32_t s_base = smem_addr(smem);
   const uint32_t q_s = s_base + C::kQOff, k_s = s_base + C::kKOff, v_s = s_base + C::kVOff;
@@ -299,180 +334,238 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
     if (lane == 0) raise_error(PA_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
+  // Tile number x of the CTA belongs to group x & 1 (not PAIR), as its tile x >> 1.
+  auto group_of = [&](int x) { return PAIR ? 0 : x & 1; };
+  auto count_of = [&](int x) { return PAIR ? x : x >> 1; };
+  // Piece number u, from the ring.
+  auto piece = [&](int u, TreePiece& c) {
+    if (!wait_use(sh.pfull[u % kTreePieces], u / kTreePieces)) return false;
+    c = sh.pieces[u % kTreePieces];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
+    return true;
+  };
 
-  if (warp == 5) {
-    // ================= TMA producer =================
-    // One cursor per ring.  Block ids of a piece's 16-token slices come in
-    // windows of 32, lane l holding slice wb + l (cur) and wb + 32 + l (nxt),
-    // and those of the next piece's first window are loaded a piece ahead, so
-    // that no load waits for a block table.
-    struct Cursor {
-      TreeWalk walk;
-      TreePiece cur, nxt;
-      bool more;  // nxt holds a piece
-      bool live;  // cur holds a tile to load
-      int i, wb, pages, pages2, first;
-    };
+  if (warp == 9) {
+    // ================= schedule, TMA producer =================
+    // Block ids of a piece's 16-token slices come in windows of 32, lane l
+    // holding slice wb + l (pages) and wb + 32 + l (pages2); the next piece,
+    // and the block ids of its first window, are looked up a piece ahead, so
+    // that no load waits for a length or a block table.
+    TreeWalk walk;
+    TreePiece cur, nxt;
+    int range = grp, u = 0, i = 0, wb = 0, pages = -1, pages2 = -1, first = -1;
+    bool more = true, live = true, ok = true;
+    int4 rec = make_int4(0, 0, 0, 0);  // the unit that starts in this range and goes on: pieces, b, g, nodes
     auto page_of = [&](const TreePiece& c, int q) {
-      const int t = c.kt0 + c.t0 * TILE + q * kSliceTokens;
-      return t < min(c.s.L, c.kt0 + c.t1 * TILE) ? p.block_tables[(int64_t)c.b * p.max_blocks + (t >> p.log2_bs)] : -1;
+      const int kt0 = c.ulo & ~(TILE - 1), t = kt0 + c.t0 * TILE + q * kSliceTokens;
+      return t < min(c.L, kt0 + c.t1 * TILE) ? p.block_tables[(int64_t)c.b * p.max_blocks + (t >> p.log2_bs)] : -1;
     };
-    auto advance = [&](Cursor& c) {  // to the next piece
-      c.cur = c.nxt;
-      c.live = c.more;
-      c.pages = c.first;
-      c.i = c.live ? c.cur.t0 : 0;
-      c.wb = 0;
-      c.pages2 = c.live ? page_of(c.cur, 32 + lane) : -1;
-      c.more = c.more && c.walk.next(p, mt, c.nxt);
-      c.first = c.more ? page_of(c.nxt, lane) : -1;
-    };
-    auto start = [&](Cursor& c) {
-      c.walk = walk;
-      c.more = c.walk.next(p, mt, c.nxt);
-      c.first = c.more ? page_of(c.nxt, lane) : -1;
-      advance(c);
-    };
-    int issued[2] = {0, 0};
-    auto issue = [&](Cursor& c, int kv) {  // the cursor's tile into its ring, as tile number issued[kv]
-      const int n = issued[kv], stage = n % (kv ? NV : NK);
-      const uint32_t full = kv ? bar(sh.vfull[stage]) : bar(sh.kfull[stage]);
-      const int rel = 4 * (c.i - c.cur.t0);
-      if (rel >= c.wb + 32) {
-        c.wb += 32;
-        c.pages = c.pages2;
-        c.pages2 = page_of(c.cur, c.wb + 32 + lane);
-      }
-      const int s = lane / C::kPanels, pn = lane % C::kPanels;  // this lane's box: slice, panel
-      const int t = c.cur.kt0 + c.i * TILE + s * kSliceTokens;
-      const int phys = __shfl_sync(FULL, c.pages, (rel + (s & 3) - c.wb) & 31);
-      const bool wanted = lane < 4 * C::kPanels && t + kSliceTokens > c.cur.ulo && t < c.cur.s.L;
-      const bool valid = wanted && phys >= 0 && phys < p.num_blocks;
-      if (kv == 0) {
-        const uint32_t bad = __ballot_sync(FULL, wanted && !valid && pn == 0);
-        if (lane == 0) {
-          uint32_t slices = 0;
-          for (int k = 0; k < 4; ++k) slices |= ((bad >> (k * C::kPanels)) & 1u) << k;
-          sh.skip[n & 15] = slices;  // read behind this tile's S, long before tile n + 16 is issued
-          if (bad) raise_error(PA_DEVERR_BLOCK);
+    auto find = [&]() {  // the next piece of this range, or of the next one claimed
+      long long at = 0;
+      while (true) {
+        if (walk.next(p, mt0 * p.q_nodes, nxt, at)) {
+          nxt.range = range;
+          if (nxt.t0 == 0 && nxt.t1 < nxt.tiles)
+            rec = make_int4(line.range_of(at + nxt.tiles - 1) - range + 1, nxt.b, nxt.g, nxt.n);
+          return true;
         }
+        if (lane < C::kRowTiles && mt0 + lane < p.m_tiles) {  // this range's record, for each row tile
+          const bool has = rec.x > 0 && (mt0 + lane) * p.q_nodes < rec.w;
+          p.ws_rec[(int64_t)range * p.m_tiles + mt0 + lane] = has ? rec : make_int4(0, 0, 0, 0);
+        }
+        rec = make_int4(0, 0, 0, 0);
+        if (line.ranges <= line.groups) return false;
+        int claim = 0;
+        if (lane == 0) claim = atomicAdd(p.queue + pair, 1);
+        range = line.groups + __shfl_sync(FULL, claim, 0);
+        if (range >= line.ranges) return false;
+        walk.start(p, sh.before, line.start(range), line.start(range + 1), lane);
       }
-      const uint32_t boxes = __popc(__ballot_sync(FULL, valid));
+    };
+    auto advance = [&]() {  // to the next piece, which goes into the ring
+      if (u >= kTreePieces && !wait_use(sh.pempty[u % kTreePieces], u / kTreePieces - 1)) return false;
+      live = more;
+      cur = nxt;
       if (lane == 0) {
-        if (boxes) mbar_arrive_expect_tx(full, boxes * kSliceTokens * 128);
-        else mbar_arrive(full);
+        if (!live) cur.b = -1;
+        sh.pieces[u % kTreePieces] = cur;
+        mbar_arrive(bar(sh.pfull[u % kTreePieces]));
       }
       __syncwarp();
-      if (valid) {
-        const uint32_t dst = (kv ? v_s : k_s) + stage * C::kKBytes + pn * C::kKVPanelBytes + s * kSliceTokens * 128;
-        const int row = (phys * p.hkv + c.cur.g) * p.block_size + (t & (p.block_size - 1));
-        tma_load_2d(dst, kv ? &vmap : &kmap, full, pn * 64, row);
-      }
-      issued[kv] = n + 1;
-      if (++c.i >= c.cur.t1) advance(c);
-    };
-    // A K stage frees when the S that read it is done, a V stage when its P V
-    // is.  The MMAs complete in issue order, S(m + 1) before P V(m) within a
-    // piece, so the refills go in that order: K(m + 1 + NK), then V(m + NV).
-    auto refill = [&](Cursor& c, int kv) {
-      const int u = issued[kv] - (kv ? NV : NK);
-      if (!wait_use(kv ? sh.vempty[u % NV] : sh.kempty[u % NK], u / (kv ? NV : NK))) return false;
-      issue(c, kv);
+      ++u;
+      if (!live) return true;
+      i = cur.t0;
+      wb = 0;
+      pages = first;
+      pages2 = page_of(cur, 32 + lane);
+      more = find();
+      first = more ? page_of(nxt, lane) : -1;
       return true;
     };
-    Cursor k, v;
-    start(k);
-    start(v);
-    for (int i = 0; i < NK && k.live; ++i) issue(k, 0);
-    for (int i = 0; i < NV && v.live; ++i) issue(v, 1);
-    bool ok = true;
-    if (k.live) ok = refill(k, 0);
-    while (ok && (k.live || v.live) && !*abort_flag) {
-      if (k.live) ok = refill(k, 0);
-      if (ok && v.live) ok = refill(v, 1);
+    int issued_k = 0, issued_v = 0;
+    auto issue_k = [&]() {  // the cursor's tile, as tile number issued_k
+      const int n = issued_k, stage = n % NK;
+      if (n >= NK && !wait_use(sh.kempty[stage], n / NK - 1)) return false;
+      const int rel = 4 * (i - cur.t0);
+      if (rel >= wb + 32) {
+        wb += 32;
+        pages = pages2;
+        pages2 = page_of(cur, wb + 32 + lane);
+      }
+      const int s = lane / C::kPanels, pn = lane % C::kPanels;  // this lane's box: slice, panel
+      const int t = (cur.ulo & ~(TILE - 1)) + i * TILE + s * kSliceTokens;
+      const int phys = __shfl_sync(FULL, pages, (rel + (s & 3) - wb) & 31);
+      const bool mine = lane < 4 * C::kPanels, wanted = mine && t + kSliceTokens > cur.ulo && t < cur.L;
+      const bool valid = wanted && phys >= 0 && phys < p.num_blocks;
+      const int row = valid ? (phys * p.hkv + cur.g) * p.block_size + (t & (p.block_size - 1)) : -1;
+      const uint32_t bad = __ballot_sync(FULL, wanted && !valid && pn == 0);
+      const uint32_t boxes = __popc(__ballot_sync(FULL, valid));
+      if (mine && pn == 0) sh.rows[n % C::kRing][s] = row;  // for V, and read long before tile n + kRing is issued
+      if (lane == 0) {
+        uint32_t slices = 0;
+        for (int k = 0; k < 4; ++k) slices |= ((bad >> (k * C::kPanels)) & 1u) << k;
+        sh.skip[n % C::kRing] = (uint8_t)slices;
+        if (bad) raise_error(PA_DEVERR_BLOCK);
+        if (boxes) mbar_arrive_expect_tx(bar(sh.kfull[stage]), boxes * kSliceTokens * 128);
+        else mbar_arrive(bar(sh.kfull[stage]));
+      }
+      __syncwarp();
+      if (valid)
+        tma_load_2d(k_s + stage * C::kKBytes + pn * C::kKVPanelBytes + s * kSliceTokens * 128, &kmap,
+                    bar(sh.kfull[stage]), pn * 64, row);
+      issued_k = n + 1;
+      if (++i >= cur.t1) return advance();
+      return true;
+    };
+    auto issue_v = [&]() {
+      const int n = issued_v, stage = n % NV;
+      if (n >= NV && !wait_use(sh.vempty[stage], n / NV - 1)) return false;
+      const int s = lane / C::kPanels, pn = lane % C::kPanels;
+      const int row = lane < 4 * C::kPanels ? sh.rows[n % C::kRing][s] : -1;
+      const uint32_t boxes = __popc(__ballot_sync(FULL, row >= 0));
+      if (lane == 0) {
+        if (boxes) mbar_arrive_expect_tx(bar(sh.vfull[stage]), boxes * kSliceTokens * 128);
+        else mbar_arrive(bar(sh.vfull[stage]));
+      }
+      __syncwarp();
+      if (row >= 0)
+        tma_load_2d(v_s + stage * C::kKBytes + pn * C::kKVPanelBytes + s * kSliceTokens * 128, &vmap,
+                    bar(sh.vfull[stage]), pn * 64, row);
+      issued_v = n + 1;
+      return true;
+    };
+    walk.start(p, sh.before, line.start(range), line.start(range + 1), lane);
+    if (blockIdx.x == 0 && lane == 0) p.ws_rec[-1].x = line.ranges;  // how many records there are
+    more = find();
+    first = more ? page_of(nxt, lane) : -1;
+    ok = advance();
+    // A K stage frees when the S that read it is done, a V stage when its P V is.
+    // P V trails S by LAG tiles, so V(j - NK + NV - LAG) goes out behind K(j).
+    constexpr int BEHIND = NK - NV + LAG;
+    while (ok && (live || issued_v < issued_k) && !*abort_flag) {
+      if (live) ok = issue_k();
+      if (ok && (issued_k - issued_v > BEHIND || (!live && issued_v < issued_k))) ok = issue_v();
     }
     if (!ok) give_up();
     if (!ok || *abort_flag) {
       // Before the CTA releases its shared memory: give the last loads of each
       // ring a bounded time to land (earlier ones have, their stages were reused).
-      for (int kv = 0; kv < 2; ++kv) {
-        const int n = kv ? NV : NK;
-        for (int j = max(issued[kv] - n, 0); j < issued[kv]; ++j)
-          (void)mbar_wait_bounded(kv ? bar(sh.vfull[j % n]) : bar(sh.kfull[j % n]), (j / n) & 1, kDrainLimitNs);
-      }
+      for (int j = max(issued_k - NK, 0); j < issued_k; ++j)
+        (void)mbar_wait_bounded(bar(sh.kfull[j % NK]), (j / NK) & 1, kDrainLimitNs);
+      for (int j = max(issued_v - NV, 0); j < issued_v; ++j)
+        (void)mbar_wait_bounded(bar(sh.vfull[j % NV]), (j / NV) & 1, kDrainLimitNs);
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ================= MMA issuer (one elected lane) =================
     const uint32_t idesc_s = umma::idesc_bf16(kTreeRows, TILE, 0, 0);
     const uint32_t idesc_o = umma::idesc_bf16(kTreeRows, D, 0, 1);
-    auto s_mma = [&](int n) {  // S(n) = Q K(n)^T into buffer n % 2
-      if (!wait_use(sh.kfull[n % NK], n / NK)) return false;
+    auto s_mma = [&](int x) {  // S = Q K(x)^T into the group's buffer (PAIR: both groups')
+      if (!wait_use(sh.kfull[x % NK], x / NK)) return false;
       umma::fence_after();
       if (umma::elect()) {
-        const uint32_t kst = k_s + (n % NK) * C::kKBytes;
+        const uint32_t kst = k_s + (x % NK) * C::kKBytes;
+        const int k = count_of(x);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t ad = umma::desc_sw128(q_s + (kk >> 2) * C::kQPanelBytes + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd = umma::desc_sw128(kst + (kk >> 2) * C::kKVPanelBytes + (kk & 3) * 32, 16, 1024);
-          umma::mma_f16(tmem + C::kSCol + (n & 1) * TILE, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+        for (int t = 0; t < C::kRowTiles; ++t) {
+          const int w = PAIR ? t : group_of(x);
+          const uint32_t col = tmem + C::kSCol + (2 * w + (k & 1)) * TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t ad =
+                umma::desc_sw128(q_s + t * C::kQBytes + (kk >> 2) * C::kQPanelBytes + (kk & 3) * 32, 16, 1024);
+            const uint64_t bd = umma::desc_sw128(kst + (kk >> 2) * C::kKVPanelBytes + (kk & 3) * 32, 16, 1024);
+            umma::mma_f16(col, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma::commit(bar(sh.sfull[w][k & 1]));
         }
-        umma::commit(bar(sh.sfull[n & 1]));
-        umma::commit(bar(sh.kempty[n % NK]));
+        umma::commit(bar(sh.kempty[x % NK]));
       }
       __syncwarp();
       return true;
     };
-    auto o_mma = [&](int n, bool first) {  // O (+)= P V(n), P in the columns of S buffer n % 2
-      if (!wait_use(sh.pready[n & 1], n >> 1) || *abort_flag) return false;
-      if (!wait_use(sh.vfull[n % NV], n / NV)) return false;
+    int begun = 0;  // pieces whose first P V was issued
+    auto o_mma = [&](int x, bool first) {  // O (+)= P V(x), P in the columns of its S buffer
+      const int k = count_of(x);
+      if (first && begun > 0 && !wait_use(sh.ofree, begun - 1)) return false;  // the last piece's O is read
+      if (first) ++begun;
+#pragma unroll
+      for (int t = 0; t < C::kRowTiles; ++t)
+        if (!wait_use(sh.pready[PAIR ? t : group_of(x)][k & 1], k >> 1)) return false;
+      if (*abort_flag || !wait_use(sh.vfull[x % NV], x / NV)) return false;
       umma::fence_after();
       if (umma::elect()) {
-        const uint32_t vst = v_s + (n % NV) * C::kKBytes;
-        const uint32_t pcol = tmem + C::kSCol + (n & 1) * TILE;
+        const uint32_t vst = v_s + (x % NV) * C::kKBytes;
 #pragma unroll
-        for (int k = 0; k < TILE / 16; ++k) {
-          const uint64_t bd = umma::desc_sw128(vst + k * 16 * 128, C::kKVPanelBytes, 1024);
-          umma::mma_f16_tmem_a(tmem + C::kOCol, pcol + k * 8, bd, idesc_o, (!first || k > 0) ? 1u : 0u);
+        for (int t = 0; t < C::kRowTiles; ++t) {
+          const int w = PAIR ? t : group_of(x);
+          const uint32_t pcol = tmem + C::kSCol + (2 * w + (k & 1)) * TILE;
+#pragma unroll
+          for (int kk = 0; kk < TILE / 16; ++kk) {
+            const uint64_t bd = umma::desc_sw128(vst + kk * 16 * 128, C::kKVPanelBytes, 1024);
+            umma::mma_f16_tmem_a(tmem + C::kOCol + t * D, pcol + kk * 8, bd, idesc_o, (!first || kk > 0) ? 1u : 0u);
+          }
+          umma::commit(bar(sh.odone[w][k & 1]));
         }
-        umma::commit(bar(sh.odone[n & 1]));
-        umma::commit(bar(sh.vempty[n % NV]));
+        umma::commit(bar(sh.vempty[x % NV]));
       }
       __syncwarp();
       return true;
     };
-    int q_issued = 0;  // Q loads issued, in the lane that issues them
-    // S of a tile goes out before P V of the tile before, except where a piece
-    // starts: its Q takes the place of the last piece's, so its first S waits
-    // for that load, and P V of the tile before does not wait for it.
-    bool ok = true, before_first = false;
-    int n = 0;
-    TreePiece c, nxt;
-    bool more = walk.next(p, mt, nxt);
-    for (int u = 0; ok && more; ++u) {
-      c = nxt;
-      for (int i = c.t0; ok && i < c.t1; ++i, ++n) {
-        if (i == c.t0) {
-          ok = n == 0 || wait_use(sh.sfull[(n - 1) & 1], (n - 1) >> 1);
+    // S of a tile goes out before P V of the tile LAG before, except where a
+    // piece starts: its Q takes the place of the last piece's, so its first S
+    // waits for that load, and P V does not wait for it.
+    bool ok = true;
+    uint32_t starts = 0;  // bit j: tile x - 1 - j is the first of its piece
+    int x = 0, q_issued = 0;
+    TreePiece c;
+    for (int u = 0; ok && (ok = piece(u, c)) && c.b >= 0; ++u) {
+      for (int i = c.t0; ok && i < c.t1; ++i, ++x) {
+        const bool first = i == c.t0;
+        auto o_before = [&]() { return x < LAG || o_mma(x - LAG, (starts >> (LAG - 1)) & 1u); };
+        if (first) {
+          ok = x == 0 || wait_use(sh.sfull[PAIR ? 1 : group_of(x - 1)][count_of(x - 1) & 1], count_of(x - 1) >> 1);
           if (!ok) break;
           if (umma::elect()) {
-            mbar_arrive_expect_tx(bar(sh.qfull), C::kPanels * p.q_nodes * G * 128);
-            for (int k = 0; k < C::kPanels; ++k)
-              tma_load_3d(q_s + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k * 64, c.g * G,
-                          c.b * p.tree_len + mt * p.q_nodes);
+            const int tiles = min(C::kRowTiles, p.m_tiles - mt0);
+            mbar_arrive_expect_tx(bar(sh.qfull), tiles * C::kPanels * p.q_nodes * G * 128);
+            for (int t = 0; t < tiles; ++t)
+              for (int k = 0; k < C::kPanels; ++k)
+                tma_load_3d(q_s + t * C::kQBytes + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k * 64, c.g * G,
+                            c.b * p.tree_len + (mt0 + t) * p.q_nodes);
             q_issued = u + 1;
           }
           __syncwarp();
-          ok = (n == 0 || o_mma(n - 1, before_first)) && wait_use(sh.qfull, u) && s_mma(n);
-          more = ok && walk.next(p, mt, nxt);
+          ok = o_before() && wait_use(sh.qfull, u) && s_mma(x);
         } else {
-          ok = s_mma(n) && o_mma(n - 1, before_first);
+          ok = s_mma(x) && o_before();
         }
-        before_first = i == c.t0;
+        starts = starts << 1 | (first ? 1u : 0u);
       }
     }
-    if (ok && n > 0) ok = o_mma(n - 1, before_first);
+    for (int y = max(x - LAG, 0); ok && y < x; ++y) ok = o_mma(y, (starts >> (x - 1 - y)) & 1u);
     if (!ok) give_up();
-    if (!ok || *abort_flag) {  // the MMAs issued get a bounded time to finish before TMEM is freed
+    if (!ok || *abort_flag) {  // the MMAs and loads issued get a bounded time to finish before TMEM is freed
       if (umma::elect()) {
         umma::commit(bar(sh.drain));
         if (q_issued > 0) (void)mbar_wait_bounded(bar(sh.qfull), (q_issued - 1) & 1, kDrainLimitNs);
@@ -480,10 +573,15 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
       (void)mbar_wait_bounded(bar(sh.drain), 0, kDrainLimitNs);
     }
   } else {
-    // ================= softmax warps 0-3: one query row per thread =================
-    const int r = tid;  // TMEM lane = row
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    // ================= softmax warps 0-7: one query row per thread =================
+    const int grp_w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;  // TMEM lane = row
+    const int mt = PAIR ? mt0 + grp_w : mt0;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t o_col = lane_base + C::kOCol + (PAIR ? grp_w * D : 0);
     const int row_stride = tree_row_stride(p);
+    const bool sectors = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // out may be aligned to 16 bytes only
+    const int node = mt * p.q_nodes + r / G;  // this thread's row: its node and its head
+    const int64_t head = (int64_t)node * p.hq + r % G;
     // Scores in the base-2 domain: x * xs, or the capped score
     // cap tanh(s / cap) log2 e = cap_a - cap_b / (1 + 2^(x cap_c)), since tanh y = 1 - 2 / (1 + e^(2 y)).
     const float xs_all = p.scale * kLog2e;
@@ -492,276 +590,324 @@ __global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, QR>::kMinBlocks)
     const float cap_a = p.softcap * kLog2e, cap_b = 2.f * cap_a;
     const float cap_c = p.use_softcap ? 2.f * xs_all / p.softcap : 0.f;
 
-    TreePiece c, nxt;
-    TreeRow row, row_nxt;
-    const int node = mt * p.q_nodes + r / G;  // this thread's row: its node and its head
-    const int64_t head = (int64_t)node * p.hq + r % G;
-    bool ok = true, more = walk.next(p, mt, nxt);
-    if (more) row_nxt = tree_row(p, nxt.s, nxt.b, node);
-    int4 rec = make_int4(0, 0, 0, 0);
-    int n = 0;
-    for (int u = 0; ok && more; ++u) {
-      c = nxt;
-      row = row_nxt;
-      const int rows = min(p.q_nodes, c.s.n - mt * p.q_nodes) * G;
-      const bool real = r < rows, active = 32 * warp < rows;
-      const int L = c.s.L, base = c.s.base;
+    // Rows of nodes that a tree does not have: no piece writes them.
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+      const TreeSeq s = tree_seq(p, b, false);
+      const int done = s.n * G, per_head = (p.tree_len * G - done) * (D / 8);
+      for (int g = 0; g < p.hkv && per_head > 0; ++g) {
+        for (int i = tid; i < per_head; i += 256) {
+          const int z = done + i / (D / 8);
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
+                             (((int64_t)b * p.tree_len + z / G) * p.hq + (int64_t)g * G + z % G) * D + i % (D / 8) * 8;
+          *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+
+    bool ok = true;
+    int x0 = 0;  // the CTA's tiles before this piece
+    TreePiece c;
+    for (int u = 0; ok && (ok = piece(u, c)) && c.b >= 0; ++u) {
+      const TreeSeq s{c.L, c.n, c.L - c.n};
+      const int rows = max(0, min(p.q_nodes, c.n - mt * p.q_nodes)) * G;
+      const bool real = r < rows, active = 32 * quad < rows;
+      const int L = c.L, base = s.base, kt0 = c.ulo & ~(TILE - 1), len = c.t1 - c.t0;
+      TreeRow row;
+      row.lo = base;
+      row.nodes = 0;
+      if (real) row = tree_row(p, s, c.b, node);
       // Rows' windows start in [ulo, ulo + 63] (a depth is at most 63) and at most at base.
       const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;
       uint64_t* bad = sh.bad[u % 3];
-      float m = -CUDART_INF_F, l = 0.f;
-      for (int i = c.t0; i < c.t1; ++i, ++n) {
-        ok = wait_use(sh.sfull[n & 1], n >> 1);
+      float m = -CUDART_INF_F, l = 0.f;  // this group's last reference, its sum
+      for (int i = PAIR ? 0 : (x0 + grp_w) & 1; i < len; i += PAIR ? 1 : 2) {
+        const int x = x0 + i, k = count_of(x);
+        ok = wait_use(sh.sfull[grp_w][k & 1], k >> 1);
         if (!ok || *abort_flag) break;
         umma::fence_after();
-        const int kt = c.kt0 + i * TILE;
-        const uint32_t skip = *const_cast<volatile uint32_t*>(&sh.skip[n & 15]);
+        const int kt = kt0 + (c.t0 + i) * TILE;
+        const uint32_t skip = *const_cast<volatile uint8_t*>(&sh.skip[x % C::kRing]);
         const bool edge = kt < w_end || kt + TILE > base;
         const bool masked = edge || kt < c.ulo || skip != 0;
-        const uint32_t s_col = lane_base + C::kSCol + (n & 1) * TILE;
+        const uint32_t s_col = lane_base + C::kSCol + (2 * grp_w + (k & 1)) * TILE;
         if (active) {
-          float x[TILE];
+          float y[TILE];
           {
-            uint32_t w[TILE / 16][16];
+            uint32_t v[TILE / 16][16];
 #pragma unroll
-            for (int k = 0; k < TILE / 16; ++k) umma::ld16_nowait(s_col + k * 16, w[k]);
+            for (int e = 0; e < TILE / 16; ++e) umma::ld16_nowait(s_col + e * 16, v[e]);
             umma::wait_ld();
 #pragma unroll
-            for (int k = 0; k < TILE; ++k) x[k] = __uint_as_float(w[k / 16][k % 16]);
+            for (int e = 0; e < TILE; ++e) y[e] = __uint_as_float(v[e / 16][e % 16]);
           }
           if (pre) {
             if (p.use_softcap) {
 #pragma unroll
-              for (int k = 0; k < TILE; ++k) {
-                float e, q;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x[k] * cap_c));
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
-                x[k] = fmaf(-cap_b, q, cap_a);
+              for (int e = 0; e < TILE; ++e) {
+                float a, q;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(y[e] * cap_c));
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + a));
+                y[e] = fmaf(-cap_b, q, cap_a);
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < TILE; ++k) x[k] *= xs_all;
+              for (int e = 0; e < TILE; ++e) y[e] *= xs_all;
             }
           }
           if (masked) {
-            // Bit k: this row attends position kt + k.
+            // Bit e: this row attends position kt + e.
             const int from = min(max(row.lo - kt, 0), TILE), to = min(max(base - kt, 0), TILE);
             uint64_t see = low_bits(to) & ~low_bits(from);
             if (kt >= base) see |= row.nodes >> (kt - base);
             else if (base - kt < TILE) see |= row.nodes << (base - kt);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if ((skip >> k) & 1u) see &= ~(0xffffull << (16 * k));
+            for (int e = 0; e < 4; ++e)
+              if ((skip >> e) & 1u) see &= ~(0xffffull << (16 * e));
             const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-            for (int k = 0; k < TILE; ++k) x[k] = ((k < 32 ? lo >> k : hi >> (k - 32)) & 1u) ? x[k] : -CUDART_INF_F;
+            for (int e = 0; e < TILE; ++e) y[e] = ((e < 32 ? lo >> e : hi >> (e - 32)) & 1u) ? y[e] : -CUDART_INF_F;
           }
           float mx[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx[k] = x[k];
+          for (int e = 0; e < 8; ++e) mx[e] = y[e];
 #pragma unroll
-          for (int k = 8; k < TILE; ++k) mx[k & 7] = fmaxf(mx[k & 7], x[k]);
-          const float mt_ = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+          for (int e = 8; e < TILE; ++e) mx[e & 7] = fmaxf(mx[e & 7], y[e]);
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * xs;  // xs > 0
-          // Lazy rescaling, as in the prefill: the reference m moves when the
+          // The reference so far: this group's, or (not PAIR) the tile's before, the other group's.
+          float before = m;
+          if (!PAIR) {
+            before = -CUDART_INF_F;
+            if (i > 0) {
+              ok = wait_use(sh.mready[quad][(x - 1) & 1], (x - 1) >> 1);
+              if (!ok) break;
+              before = sh.m[(x - 1) & 1][r];
+            }
+          }
+          // Lazy rescaling, as in the prefill: the reference moves when the
           // tile's maximum exceeds it by more than 8 (base 2), so weights stay
           // below 256 and share the reference of the sum and of O.
-          const float mn = (m == -CUDART_INF_F || mt_ > m + 8.f) ? mt_ : m;
-          const float ref = mn == -CUDART_INF_F ? 0.f : mn;
-          const float alpha = exp2f(m - ref);
-          const bool moved = mn != m;
-          m = mn;
+          const float now = (before == -CUDART_INF_F || top > before + 8.f) ? top : before;
+          if (!PAIR) {
+            sh.m[x & 1][r] = now;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh.mready[quad][x & 1]));
+          }
+          const float ref = now == -CUDART_INF_F ? 0.f : now;
+          l *= exp2f(m - ref);
+          m = now;
           // Weights in fp32 for the sum, rounded to bf16 for the second product
           // (a relative 2^-8 at most on each weight, what the output's own
           // rounding allows; the tensor cores take both operands in one type).
           float ps[4] = {0.f, 0.f, 0.f, 0.f};
           uint32_t pk[TILE / 2];
 #pragma unroll
-          for (int k = 0; k < TILE / 2; ++k) {
+          for (int e = 0; e < TILE / 2; ++e) {
             float e0, e1;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fmaf(x[2 * k], xs, -ref)));
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fmaf(x[2 * k + 1], xs, -ref)));
-            ps[k & 3] += e0 + e1;
-            pk[k] = pack_bf16x2(e0, e1);
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fmaf(y[2 * e], xs, -ref)));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fmaf(y[2 * e + 1], xs, -ref)));
+            ps[e & 3] += e0 + e1;
+            pk[e] = pack_bf16x2(e0, e1);
           }
-          l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
           umma::st16_nowait(s_col, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
           umma::st16_nowait(s_col + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
           // (The first tile's P V overwrites O; rows that nobody reads move nothing.)
-          if (i > c.t0 && __any_sync(FULL, moved && real)) {
-            ok = wait_use(sh.odone[(n - 1) & 1], (n - 1) >> 1);
+          if (i > 0 && __any_sync(FULL, now != before && real)) {
+            const float alpha = exp2f(before - ref);
+            const int w = PAIR ? grp_w : group_of(x - 1), kb = count_of(x - 1);
+            ok = wait_use(sh.odone[w][kb & 1], kb >> 1);
             if (!ok) break;
             umma::fence_after();
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
+            for (int e = 0; e < D / 16; ++e) {
               float v[16];
-              umma::ld16(lane_base + C::kOCol + k * 16, v);
+              umma::ld16(o_col + e * 16, v);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] *= alpha;
-              umma::st16(lane_base + C::kOCol + k * 16, v);
+              for (int j = 0; j < 16; ++j) v[j] *= alpha;
+              umma::st16(o_col + e * 16, v);
             }
           }
           umma::wait_st();
+        } else if (!PAIR && lane == 0) {
+          mbar_arrive(bar(sh.mready[quad][x & 1]));  // one arrival a tile, whoever reads
         }
         if (masked) {
-          ok = wait_use(sh.vfull[n % NV], n / NV);
+          ok = wait_use(sh.vfull[x % NV], x / NV);
           if (!ok) break;
-          const uint32_t vst = v_s + (n % NV) * C::kKBytes;
+          const uint32_t vst = v_s + (x % NV) * C::kKBytes;
           constexpr int CPR = C::kPanels * 8;  // 16-byte chunks of a row
-          auto chunk = [&](int idx) {          // row idx / CPR; where a row's chunks are does not matter
-            const int k = idx / CPR, rem = idx % CPR;
-            return vst + (rem >> 3) * C::kKVPanelBytes + k * 128 + ((rem & 7) << 4);
+          constexpr int NT = PAIR ? 256 : 128;  // threads at it
+          const int me = PAIR ? tid : tid & 127;
+          auto chunk = [&](int idx) {  // of row idx / CPR; where a row's chunks are does not matter
+            const int e = idx / CPR, rem = idx % CPR;
+            return vst + (rem >> 3) * C::kKVPanelBytes + e * 128 + ((rem & 7) << 4);
           };
           // Rows of V that no row attends: zero (they were not loaded, or hold what stands behind the end).
           uint64_t none = low_bits(min(max(c.ulo - kt, 0), TILE)) | ~low_bits(min(max(L - kt, 0), TILE));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((skip >> k) & 1u) none |= 0xffffull << (16 * k);
+          for (int e = 0; e < 4; ++e)
+            if ((skip >> e) & 1u) none |= 0xffffull << (16 * e);
           if (none) {
-            for (int idx = tid; idx < TILE * CPR; idx += 128)
+            for (int idx = me; idx < TILE * CPR; idx += NT)
               if ((none >> (idx / CPR)) & 1ull)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(idx)), "r"(0u) : "memory");
           }
           if (edge) {
-            const int slot = kt + TILE > base ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - c.kt0) / TILE;
-            constexpr int U = 4;
+            const int slot = kt + TILE > base ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - kt0) / TILE;
+            constexpr int U = TILE * CPR / NT < 4 ? TILE * CPR / NT : 4;
 #pragma unroll 1
-            for (int i0 = tid; i0 < TILE * CPR; i0 += 128 * U) {
-              uint32_t w[U][4], top = 0;
+            for (int i0 = me; i0 < TILE * CPR; i0 += NT * U) {
+              uint32_t v[U][4], exps = 0;
 #pragma unroll
               for (int e = 0; e < U; ++e)
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
-                             : "r"(chunk(i0 + 128 * e)));
+                             : "=r"(v[e][0]), "=r"(v[e][1]), "=r"(v[e][2]), "=r"(v[e][3])
+                             : "r"(chunk(i0 + NT * e)));
 #pragma unroll
               for (int e = 0; e < U; ++e)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[e][j] & 0x7f807f80u);
+                for (int j = 0; j < 4; ++j) exps = __vmaxu2(exps, v[e][j] & 0x7f807f80u);
               // Exponent bits all set in some element: not finite.  (Rows just
               // zeroed by another thread may still read as what stood there.)
-              if ((top & 0xffffu) != 0x7f80u && (top >> 16) != 0x7f80u) continue;
+              if ((exps & 0xffffu) != 0x7f80u && (exps >> 16) != 0x7f80u) continue;
               for (int e = 0; e < U; ++e) {
-                const int idx = i0 + 128 * e, k = idx / CPR;
-                if ((none >> k) & 1ull) continue;
+                const int idx = i0 + NT * e, at = idx / CPR;
+                if ((none >> at) & 1ull) continue;
                 bool found = false;
                 for (int j = 0; j < 4; ++j) {
-                  if ((w[e][j] & 0x7f80u) == 0x7f80u) w[e][j] &= 0xffff0000u, found = true;
-                  if ((w[e][j] & 0x7f800000u) == 0x7f800000u) w[e][j] &= 0xffffu, found = true;
+                  if ((v[e][j] & 0x7f80u) == 0x7f80u) v[e][j] &= 0xffff0000u, found = true;
+                  if ((v[e][j] & 0x7f800000u) == 0x7f800000u) v[e][j] &= 0xffffu, found = true;
                 }
                 if (!found) continue;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(idx)), "r"(w[e][0]),
-                             "r"(w[e][1]), "r"(w[e][2]), "r"(w[e][3])
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(idx)), "r"(v[e][0]),
+                             "r"(v[e][1]), "r"(v[e][2]), "r"(v[e][3])
                              : "memory");
-                atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << k);
+                atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << at);
               }
             }
           }
           fence_proxy_async_smem();  // visible to the tensor core's reads
         }
-        // The next piece's marks, clear before any warp can be at that piece
-        // and after every warp is past the piece that used them (three ago).
-        if (i == c.t1 - 1 && tid < 4) sh.bad[(u + 1) % 3][tid] = 0;
         umma::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.pready[n & 1]));
-        if (i == c.t0) {  // the next piece, while the tensor core is at this one
-          more = walk.next(p, mt, nxt);
-          if (more) row_nxt = tree_row(p, nxt.s, nxt.b, node);
-        }
+        if (lane == 0) mbar_arrive(bar(sh.pready[grp_w][k & 1]));
       }
       if (!ok || *abort_flag) break;
 
       // ---- write the piece's rows -------------------------------------------------------
-      const bool begins = c.t0 == 0, ends = c.t1 == c.tiles;
-      ok = wait_use(sh.odone[(n - 1) & 1], (n - 1) >> 1);
+      const int last = x0 + len - 1, kl = count_of(last);
+      x0 += len;
+      float fin = m;  // the reference of the piece's last tile
+      if (!PAIR && active && group_of(last) != grp_w) {
+        ok = wait_use(sh.mready[quad][last & 1], last >> 1);
+        if (!ok) break;
+        fin = sh.m[last & 1][r];
+      }
+      if (!PAIR) l *= exp2f(m - (fin == -CUDART_INF_F ? 0.f : fin));
+      ok = wait_use(sh.odone[PAIR ? grp_w : group_of(last)][kl & 1], kl >> 1);
       if (!ok) break;
       umma::fence_after();
+      if (!PAIR && active) sh.l[grp_w][r] = l;
+      // The next piece's marks, clear before any warp can be at that piece and
+      // after every warp is past the piece that used them (three ago).
+      if (tid < 4) sh.bad[(u + 1) % 3][tid] = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.epi));
+      ok = wait_use(sh.epi, u);
+      if (!ok) break;
+      if (!PAIR && active) l = sh.l[0][r] + sh.l[1][r];
       uint64_t marks = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) marks |= *const_cast<volatile uint64_t*>(&bad[k]);
-      const bool fin = begins && ends;
+      for (int e = 0; e < 4; ++e) marks |= *const_cast<volatile uint64_t*>(&bad[e]);
+      const bool begins = c.t0 == 0, whole = begins && c.t1 == c.tiles;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-      float* po = p.ws_o + (int64_t)slot * row_stride * D + r * 4;
+      const int64_t slot = ((int64_t)c.range * p.m_tiles + mt) * 2 + (begins ? 1 : 0);
+      float* po = p.ws_o + slot * row_stride * D + r * 4;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                             ((int64_t)c.b * p.tree_len * p.hq + (int64_t)c.g * G + head) * D;
       if (active) {
+        // Not PAIR: each group writes half of the columns.
+        const int e0 = PAIR ? 0 : grp_w * (D / 32), e1 = PAIR ? D / 16 : e0 + D / 32;
 #pragma unroll 2
-        for (int k = 0; k < D / 16; ++k) {
+        for (int e = e0; e < e1; ++e) {
           float v[16];
-          umma::ld16(lane_base + C::kOCol + k * 16, v);
+          umma::ld16(o_col + e * 16, v);
           if (marks && real) {  // give back what was taken out of V, to a row that attends it
-            for (int e = 0; e < 4; ++e) {
-              uint64_t b = bad[e];
-              const int kt = e < 2 ? c.kt0 + e * TILE : (base & ~(TILE - 1)) + (e - 2) * TILE;
-              while (b) {
-                const int t = kt + __ffsll((long long)b) - 1;
-                b &= b - 1;
+            for (int z = 0; z < 4; ++z) {
+              uint64_t rest = bad[z];
+              const int kt = z < 2 ? kt0 + z * TILE : (base & ~(TILE - 1)) + (z - 2) * TILE;
+              while (rest) {
+                const int t = kt + __ffsll((long long)rest) - 1;
+                rest &= rest - 1;
                 if (t < base ? t < row.lo : !((row.nodes >> (t - base)) & 1ull)) continue;
                 const int phys = p.block_tables[(int64_t)c.b * p.max_blocks + (t >> p.log2_bs)];
                 const __nv_bfloat16* src =
                     static_cast<const __nv_bfloat16*>(p.v_cache) +
-                    (((int64_t)phys * p.hkv + c.g) * p.block_size + (t & (p.block_size - 1))) * D + k * 16;
+                    (((int64_t)phys * p.hkv + c.g) * p.block_size + (t & (p.block_size - 1))) * D + e * 16;
                 for (int j = 0; j < 16; ++j) {
-                  const float y = __bfloat162float(src[j]);
-                  if (!isfinite(y)) v[j] += y;
+                  const float f = __bfloat162float(src[j]);
+                  if (!isfinite(f)) v[j] += f;
                 }
               }
             }
           }
           if (!real) continue;
-          if (fin) {
-            uint4 a, b;
-            a.x = pack_bf16x2(v[0] * inv, v[1] * inv);
-            a.y = pack_bf16x2(v[2] * inv, v[3] * inv);
-            a.z = pack_bf16x2(v[4] * inv, v[5] * inv);
-            a.w = pack_bf16x2(v[6] * inv, v[7] * inv);
-            b.x = pack_bf16x2(v[8] * inv, v[9] * inv);
-            b.y = pack_bf16x2(v[10] * inv, v[11] * inv);
-            b.z = pack_bf16x2(v[12] * inv, v[13] * inv);
-            b.w = pack_bf16x2(v[14] * inv, v[15] * inv);
-            reinterpret_cast<uint4*>(orow + k * 16)[0] = a;
-            reinterpret_cast<uint4*>(orow + k * 16)[1] = b;
+          if (whole) {
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+            if (sectors) {
+              st_global_32(orow + e * 16, o);
+            } else {
+              reinterpret_cast<uint4*>(orow + e * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              reinterpret_cast<uint4*>(orow + e * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(po + (int64_t)(k * 4 + e) * row_stride * 4) =
-                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(po + (int64_t)(e * 4 + j) * row_stride * 4) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
         }
-        if (real && !fin) *reinterpret_cast<float2*>(p.ws_ml + ((int64_t)slot * row_stride + r) * 2) = make_float2(m, l);
+        if (real && !whole && (PAIR || grp_w == 0))
+          *reinterpret_cast<float2*>(p.ws_ml + (slot * row_stride + r) * 2) = make_float2(fin, l);
       }
-      if (begins && !ends)  // goes on in the next ranges: joined by the combine
-        rec = make_int4((int)((c.start + c.tiles - 1) / sh.per) - grp + 1, c.b, c.g, rows);
+      umma::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.ofree));
     }
     if (!ok) give_up();
-    if (tid == 0) p.ws_rec[blockIdx.x] = ok && !*abort_flag ? rec : make_int4(0, 0, 0, 0);
   }
   // Every tcgen05 access is complete (waited); free the tensor memory.
   umma::fence_before();
   __syncthreads();
   if (warp == 0) {
     umma::fence_after();
-    umma::dealloc(tmem, C::kTmemCols);
+    umma::dealloc(tmem, 512);
   }
 }
 
-// Joins the pieces of each unit that was cut: CTA blockIdx.x of the attention
-// grid holds its first piece (slot 1) and says how many there are; the others
-// are in slot 0 of the next CTAs of the same row tile.  With M = max m_p:
+// Joins the pieces of each unit that was cut.  blockIdx.x: a record, of range c
+// and row tile t: the unit whose first piece is in c (slot 1) and that goes on;
+// the other pieces are in slot 0 of the next ranges.  With M = max m_p:
 //   out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,
 // in piece order.  blockIdx.y: 8 rows; a thread has four columns of one row,
 // and neighbouring threads neighbouring rows, as the partials lie.
 template <int D>
 __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p) {
   pdl_wait();  // the partials come from the attention grid
-  const int c = blockIdx.x;
-  const int4 rec = p.ws_rec[c];
-  const int r = blockIdx.y * kTreeCombineRows + (threadIdx.x & (kTreeCombineRows - 1));
-  const int col4 = threadIdx.x / kTreeCombineRows;
-  if (rec.x == 0 || r >= rec.w) return;
-  const int row_stride = tree_row_stride(p), G = p.group, node = c % p.m_tiles * p.q_nodes + r / G;
-  auto slot = [&](int k) { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k * p.m_tiles)); };
+  const int c = blockIdx.x / p.m_tiles, t = blockIdx.x - c * p.m_tiles;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kTreeMaxPairs) p.queue[threadIdx.x] = 0;  // for the next call
+  const int ranges = p.ws_rec[-1].x;
+  const int4 rec = p.ws_rec[blockIdx.x];
+  if (c >= ranges || rec.x < 2 || c + rec.x > ranges) return;
+  const int G = p.group, r = blockIdx.y * kTreeCombineRows + (threadIdx.x & (kTreeCombineRows - 1));
+  const int node = t * p.q_nodes + r / G;
+  if (r >= p.q_nodes * G || node >= min(rec.w, p.tree_len)) return;
+  if ((unsigned)rec.y >= (unsigned)p.batch || (unsigned)rec.z >= (unsigned)p.hkv) return;  // left by a call that gave up
+  const int col4 = threadIdx.x / kTreeCombineRows, row_stride = tree_row_stride(p);
+  auto slot = [&](int k) { return ((int64_t)(c + k) * p.m_tiles + t) * 2 + (k == 0 ? 1 : 0); };
   float M = -CUDART_INF_F;
   for (int k = 0; k < rec.x; ++k) M = fmaxf(M, p.ws_ml[(slot(k) * row_stride + r) * 2]);
   const float ref = M == -CUDART_INF_F ? 0.f : M;

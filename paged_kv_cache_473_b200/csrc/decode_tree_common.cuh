@@ -29,7 +29,8 @@ struct TreeParams {
   int64_t mask_stride;          // 0: every sequence has the same tree
   float* ws_o;                  // partials (decode_tree.cuh)
   float* ws_ml;
-  int4* ws_rec;
+  int4* ws_rec;                 // one record per (range, row tile); ws_rec[-1].x: how many ranges there are
+  int* queue;                   // ranges claimed, for each CTA of a group (zero between calls)
   int batch, tree_len, hq, hkv, group;
   int block_size, log2_bs, max_blocks, num_blocks;
   int window, max_context;

@@ -100,25 +100,29 @@ cudaError_t launch_tree_simt(const TreeParams& p, int head_dim, cudaStream_t st)
   }
 }
 
-// How the tensor-core kernel takes a call.  A row tile is a whole number of
-// nodes; the grid is all CTAs that are resident at once, a whole number of
-// groups of m_tiles.  Workspace: the counter region of the split-K calls
-// (untouched), one record per CTA, two partials of `rows` rows per CTA.
+// How the tensor-core kernel takes a call: one CTA per SM, for one row tile of
+// whole nodes or (head_dim 64 and 128, where tensor memory holds two outputs)
+// for two of them.  Workspace: the counter region of the split-K calls, whose
+// first words count the claimed ranges, one record per (range, row tile) behind
+// a header, two partials of `rows` rows for each.
 struct TreePlan {
-  int q_nodes, m_tiles, grid, rows;
+  int q_nodes, m_tiles, grid, rows, records;
+  bool pair;
   size_t rec, o, ml, bytes;
 };
 TreePlan tree_plan(int head_dim, int tree_len, int group) {
   TreePlan w;
   w.q_nodes = std::min(tree_len, pa::kTreeRows / group);
   w.m_tiles = (tree_len + w.q_nodes - 1) / w.q_nodes;
-  const int per_sm = head_dim <= 128 ? pa::TreeCfg<128, 128>::kMinBlocks : pa::TreeCfg<256, 128>::kMinBlocks;
-  w.grid = std::max(1, sm_count() * per_sm / w.m_tiles) * w.m_tiles;
+  w.pair = w.m_tiles > 1 && head_dim <= 128;
+  const int share = w.pair ? (w.m_tiles + 1) / 2 : w.m_tiles;  // CTAs that take the same range
+  w.grid = std::max(1, sm_count() / share) * share;
   w.rows = (w.q_nodes * group + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows * pa::kTreeCombineRows;
-  w.rec = pa::kCounterBytes;
-  w.o = w.rec + align256((size_t)w.grid * sizeof(int4));
-  w.ml = w.o + align256(2 * (size_t)w.grid * w.rows * head_dim * 4);
-  w.bytes = w.ml + align256(2 * (size_t)w.grid * w.rows * 2 * 4);
+  w.records = w.grid / share * (1 + pa::kTreeClaimsPerCta) * w.m_tiles;
+  w.rec = pa::kCounterBytes + 256;
+  w.o = w.rec + align256((size_t)w.records * sizeof(int4));
+  w.ml = w.o + align256(2 * (size_t)w.records * w.rows * head_dim * 4);
+  w.bytes = w.ml + align256(2 * (size_t)w.records * w.rows * 2 * 4);
   return w;
 }
 
@@ -134,33 +138,34 @@ bool encode_q_map(CUtensorMap* map, const TreeParams& p, int head_dim) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int QR>
+template <int D, int QR, bool PAIR>
 cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t st) {
-  using Cfg = pa::TreeCfg<D, QR>;
+  using Cfg = pa::TreeCfg<D, QR, PAIR>;
   CUtensorMap qmap, kmap, vmap;
   const long long rows = (long long)p.num_blocks * p.hkv * p.block_size;
   if (!tensor_map_encoder() || !encode_q_map(&qmap, p, D) || !encode_cache_map(&kmap, p.k_cache, D, rows) ||
       !encode_cache_map(&vmap, p.v_cache, D, rows))
     return cudaErrorInvalidValue;
-  auto kern = pa::decode_tree_kernel<D, QR>;
+  auto kern = pa::decode_tree_kernel<D, QR, PAIR>;
   static std::atomic<uint64_t> smem_done{0};
   cudaError_t e = set_smem(kern, Cfg::kSmemBytes, smem_done);
   if (e != cudaSuccess) return e;
   e = launch_ex(kern, dim3(w.grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  return launch_ex(pa::tree_combine_kernel<D>, dim3(w.grid, w.rows / pa::kTreeCombineRows), dim3(2 * D), 0, st, true,
-                   p);
+  return launch_ex(pa::tree_combine_kernel<D>, dim3(w.records, w.rows / pa::kTreeCombineRows), dim3(2 * D), 0, st,
+                   true, p);
 }
 
 cudaError_t launch_tree(const TreeParams& p, int head_dim, const TreePlan& w, cudaStream_t st) {
   const bool small = w.rows <= 64;
   switch (head_dim) {
     case 64:
-      return launch_tree_t<64, 128>(p, w, st);
+      return w.pair ? launch_tree_t<64, 128, true>(p, w, st) : launch_tree_t<64, 128, false>(p, w, st);
     case 128:
-      return small ? launch_tree_t<128, 64>(p, w, st) : launch_tree_t<128, 128>(p, w, st);
+      if (w.pair) return launch_tree_t<128, 128, true>(p, w, st);
+      return small ? launch_tree_t<128, 64, false>(p, w, st) : launch_tree_t<128, 128, false>(p, w, st);
     default:
-      return small ? launch_tree_t<256, 64>(p, w, st) : launch_tree_t<256, 128>(p, w, st);
+      return small ? launch_tree_t<256, 64, false>(p, w, st) : launch_tree_t<256, 128, false>(p, w, st);
   }
 }
 
@@ -316,6 +321,7 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
     return PA_OK;
   }
   char* ws = static_cast<char*>(workspace);
+  p.queue = reinterpret_cast<int*>(ws);
   p.ws_rec = reinterpret_cast<int4*>(ws + w.rec);
   p.ws_o = reinterpret_cast<float*>(ws + w.o);
   p.ws_ml = reinterpret_cast<float*>(ws + w.ml);

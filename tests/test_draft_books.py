@@ -76,7 +76,7 @@ def test_tree_workspace_size():
     one = pa.decode_tree_workspace_size(1, 1, 32, 128, 1024, 8)
     assert 256 * 1024 < one < pa.decode_tree_workspace_size(1, 8, 32, 128, 1024, 8)
     most = pa.decode_tree_workspace_size(1, 32, 32, 128, 1024, 8)
-    assert pa.decode_tree_workspace_size(500, 64, 32, 128, 1 << 20, 8) <= most < 64 << 20
+    assert pa.decode_tree_workspace_size(500, 64, 32, 128, 1 << 20, 8) <= 2 * most < 256 << 20
     for bad in ((0, 4, 8, 64, 10, 2), (1, 0, 8, 64, 10, 2), (1, 65, 8, 64, 10, 2), (1, 4, 9, 64, 10, 2), (1, 4, 18, 64, 10, 2)):
         assert pa.decode_tree_workspace_size(*bad) == 0
     args = dict(TREE[1], wsb=pa.decode_tree_workspace_size(2, 16, 8, 128, 64, 2) - 1)

@@ -256,6 +256,24 @@ def test_where_the_blocks_lie_does_not_matter(dtype):
         assert torch.equal(bits(_run(c, workspace=ws)), bits(out))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tensors_aligned_to_16_bytes_only(dtype):
+    """q, out and the caches 16 bytes off a larger alignment: the same bits."""
+    c = _case([100, 333, 64, 17], 10, (32, 8, 128), dtype, seed=25)
+    want = _run(c)
+    skip = 16 // c["q"].element_size()
+
+    def off(t):
+        flat = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+        view = flat[skip:skip + t.numel()].view(t.shape)
+        assert view.data_ptr() % 32 == 16
+        return view.copy_(t)
+
+    moved = dict(c, q=off(c["q"]), k_cache=off(c["k_cache"]), v_cache=off(c["v_cache"]))
+    out = off(torch.zeros_like(c["q"]))
+    assert torch.equal(bits(_run(moved, out=out)), bits(want))
+
+
 def test_many_short_sequences():
     """More sequences than threads in a CTA, most of them a tile or less, some empty."""
     g = torch.Generator().manual_seed(4)
