@@ -34,8 +34,10 @@
 // Warps 0-7: softmax, one row per thread; they also write the rows.  Warp 8: MMA
 // issue, and the load of a piece's Q as soon as the last S of the piece before
 // is done.  Warp 9: the schedule (pieces go to the other warps through a ring in
-// shared memory) and the TMA loads of K and V (16-row boxes, one per lane).  Every wait
-// is bounded; a wait that gives up raises the abort flag, which ends all roles.
+// shared memory) and the TMA loads of K; warp 10: those of V (boxes of 64 columns and
+// as many rows as lie together, a block's up to 64, all issued by one lane).
+// Every wait is bounded; a wait that gives up raises the abort flag, which ends all
+// roles.
 //
 // Masks.  A tile is masked where it reaches before a row's window, into the
 // tree or past the sequence's end, or where a block id is bad; there each
@@ -56,7 +58,7 @@ namespace pa {
 
 constexpr int kTreeRows = 128;  // query rows per row tile (UMMA M)
 constexpr int kTreeTile = 64;   // keys per tile
-constexpr int kTreeWarps = 10;
+constexpr int kTreeWarps = 11;
 constexpr int kTreeThreads = kTreeWarps * 32;
 constexpr int kTreeCombineRows = 8;
 constexpr int kTreeMinTiles = 2;    // shortest range: below, a piece's fixed cost outweighs its tiles
@@ -91,7 +93,7 @@ struct TreeCfg {
   static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
   static constexpr int kSCol = 256;                     // four S buffers, two per group
   static_assert(!PAIR || D <= 128, "tensor memory");
-  static_assert(kKStages + kLag + 1 < kRing, "ring");
+  static_assert(kKStages + kLag + 1 < kRing && kVStages + kLag + 1 < kRing, "ring");
 };
 
 // A piece: tiles [t0, t1) of the `tiles` tiles of unit (b, g).  b < 0: no more.
@@ -109,11 +111,12 @@ struct TreeShared {
   uint64_t sfull[2][2], pready[2][2], odone[2][2];  // [group][buffer]
   uint64_t mready[4][2];                            // [warp of the group][tile parity]
   uint64_t pfull[kTreePieces], pempty[kTreePieces];
+  uint64_t rfull[C::kRing];                         // rows[] of a tile are written
   uint64_t qfull, epi, ofree, drain;
   uint64_t bad[3][4];  // by piece: rows of V with elements that are not finite, in each masked tile
   TreePiece pieces[kTreePieces];
-  int rows[C::kRing][4];   // by tile: cache rows of its slices (-1: not loaded)
-  uint8_t skip[C::kRing];  // by tile: slices whose block id is bad
+  alignas(16) int rows[C::kRing][4];  // by tile: cache rows of its boxes (-1: not loaded; -2: no more tiles)
+  uint8_t skip[C::kRing];  // by tile: 16-row slices whose block id is bad
   float m[PAIR ? 1 : 2][PAIR ? 1 : QR];  // running maximum, by tile parity
   float l[PAIR ? 1 : 2][PAIR ? 1 : QR];  // the groups' sums at a piece's end
   long long before[kTreeWarps + 1];      // tiles before each tenth of the batch
@@ -258,6 +261,20 @@ __device__ __forceinline__ int tree_row_stride(const TreeParams& p) {
   return (p.q_nodes * p.group + kTreeCombineRows - 1) & ~(kTreeCombineRows - 1);
 }
 
+// One lane: a tile's boxes, of `box_rows` cache rows from row0, row1, ... on (-1: none), into its panels at dst.
+template <int PANELS>
+__device__ __forceinline__ void tree_load_boxes(uint32_t dst, const CUtensorMap* map, uint32_t full, int row0, int row1,
+                                                int row2, int row3, int box_rows) {
+  const int rows[4] = {row0, row1, row2, row3};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (rows[k] < 0) continue;
+#pragma unroll
+    for (int pn = 0; pn < PANELS; ++pn)
+      tma_load_2d(dst + pn * kTreeTile * 128 + k * box_rows * 128, map, full, pn * 64, rows[k]);
+  }
+}
+
 template <int D, int QR, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -294,6 +311,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mbar_init(bar(sh.pfull[s]), 1);
       mbar_init(bar(sh.pempty[s]), 9);  // the MMA warp and the softmax warps
     }
+    for (int s = 0; s < C::kRing; ++s) mbar_init(bar(sh.rfull[s]), 1);
     mbar_init(bar(sh.qfull), 1);
     mbar_init(bar(sh.epi), 8);
     mbar_init(bar(sh.ofree), 8);
@@ -337,28 +355,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // Tile number x of the CTA belongs to group x & 1 (not PAIR), as its tile x >> 1.
   auto group_of = [&](int x) { return PAIR ? 0 : x & 1; };
   auto count_of = [&](int x) { return PAIR ? x : x >> 1; };
-  // Piece number u, from the ring.
-  auto piece = [&](int u, TreePiece& c) {
-    if (!wait_use(sh.pfull[u % kTreePieces], u / kTreePieces)) return false;
-    c = sh.pieces[u % kTreePieces];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
-    return true;
-  };
 
   if (warp == 9) {
-    // ================= schedule, TMA producer =================
-    // Block ids of a piece's 16-token slices come in windows of 32, lane l
-    // holding slice wb + l (pages) and wb + 32 + l (pages2); the next piece,
-    // and the block ids of its first window, are looked up a piece ahead, so
-    // that no load waits for a length or a block table.
+    // ================= schedule, TMA loads of K =================
+    // Block ids of a piece's boxes come in windows of 32, lane l holding box
+    // wb + l (pages) and wb + 32 + l (pages2); the next piece, and the block ids
+    // of its first window, are looked up a piece ahead, so that no load waits
+    // for a length or a block table.
     TreeWalk walk;
     TreePiece cur, nxt;
     int range = grp, u = 0, i = 0, wb = 0, pages = -1, pages2 = -1, first = -1;
     bool more = true, live = true, ok = true;
     int4 rec = make_int4(0, 0, 0, 0);  // the unit that starts in this range and goes on: pieces, b, g, nodes
     auto page_of = [&](const TreePiece& c, int q) {
-      const int kt0 = c.ulo & ~(TILE - 1), t = kt0 + c.t0 * TILE + q * kSliceTokens;
+      const int kt0 = c.ulo & ~(TILE - 1), t = kt0 + c.t0 * TILE + (q << p.log2_box);
       return t < min(c.L, kt0 + c.t1 * TILE) ? p.block_tables[(int64_t)c.b * p.max_blocks + (t >> p.log2_bs)] : -1;
     };
     auto find = [&]() {  // the next piece of this range, or of the next one claimed
@@ -403,56 +413,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       first = more ? page_of(nxt, lane) : -1;
       return true;
     };
-    int issued_k = 0, issued_v = 0;
-    auto issue_k = [&]() {  // the cursor's tile, as tile number issued_k
-      const int n = issued_k, stage = n % NK;
+    const int boxes = TILE >> p.log2_box, box_rows = 1 << p.log2_box;  // of a tile: 4, 2 or 1
+    int issued = 0;
+    auto issue = [&]() {  // the cursor's tile, as tile number `issued`
+      const int n = issued, stage = n % NK, at = n % C::kRing;
       if (n >= NK && !wait_use(sh.kempty[stage], n / NK - 1)) return false;
-      const int rel = 4 * (i - cur.t0);
+      const int rel = boxes * (i - cur.t0);
       if (rel >= wb + 32) {
         wb += 32;
         pages = pages2;
         pages2 = page_of(cur, wb + 32 + lane);
       }
-      const int s = lane / C::kPanels, pn = lane % C::kPanels;  // this lane's box: slice, panel
-      const int t = (cur.ulo & ~(TILE - 1)) + i * TILE + s * kSliceTokens;
-      const int phys = __shfl_sync(FULL, pages, (rel + (s & 3) - wb) & 31);
-      const bool mine = lane < 4 * C::kPanels, wanted = mine && t + kSliceTokens > cur.ulo && t < cur.L;
+      const int t = (cur.ulo & ~(TILE - 1)) + i * TILE + (lane << p.log2_box);  // lane: box
+      const int phys = __shfl_sync(FULL, pages, (rel + (lane & (boxes - 1)) - wb) & 31);
+      const bool wanted = lane < boxes && t + box_rows > cur.ulo && t < cur.L;
       const bool valid = wanted && phys >= 0 && phys < p.num_blocks;
       const int row = valid ? (phys * p.hkv + cur.g) * p.block_size + (t & (p.block_size - 1)) : -1;
-      const uint32_t bad = __ballot_sync(FULL, wanted && !valid && pn == 0);
-      const uint32_t boxes = __popc(__ballot_sync(FULL, valid));
-      if (mine && pn == 0) sh.rows[n % C::kRing][s] = row;  // for V, and read long before tile n + kRing is issued
-      if (lane == 0) {
+      const uint32_t bad = __ballot_sync(FULL, wanted && !valid), good = __ballot_sync(FULL, valid);
+      if (lane < 4) sh.rows[at][lane] = row;  // for V; read long before tile n + kRing is issued
+      const int row0 = __shfl_sync(FULL, row, 0), row1 = __shfl_sync(FULL, row, 1);
+      const int row2 = __shfl_sync(FULL, row, 2), row3 = __shfl_sync(FULL, row, 3);
+      if (umma::elect()) {
         uint32_t slices = 0;
-        for (int k = 0; k < 4; ++k) slices |= ((bad >> (k * C::kPanels)) & 1u) << k;
-        sh.skip[n % C::kRing] = (uint8_t)slices;
+        for (int k = 0; k < 4; ++k) slices |= ((bad >> (k * kSliceTokens >> p.log2_box)) & 1u) << k;
+        sh.skip[at] = (uint8_t)slices;
         if (bad) raise_error(PA_DEVERR_BLOCK);
-        if (boxes) mbar_arrive_expect_tx(bar(sh.kfull[stage]), boxes * kSliceTokens * 128);
-        else mbar_arrive(bar(sh.kfull[stage]));
+        const uint32_t full = bar(sh.kfull[stage]), dst = k_s + stage * C::kKBytes;
+        if (good) mbar_arrive_expect_tx(full, __popc(good) * C::kPanels * box_rows * 128);
+        else mbar_arrive(full);
+        tree_load_boxes<C::kPanels>(dst, &kmap, full, row0, row1, row2, row3, box_rows);
       }
       __syncwarp();
-      if (valid)
-        tma_load_2d(k_s + stage * C::kKBytes + pn * C::kKVPanelBytes + s * kSliceTokens * 128, &kmap,
-                    bar(sh.kfull[stage]), pn * 64, row);
-      issued_k = n + 1;
+      if (lane == 0) mbar_arrive(bar(sh.rfull[at]));
+      issued = n + 1;
       if (++i >= cur.t1) return advance();
-      return true;
-    };
-    auto issue_v = [&]() {
-      const int n = issued_v, stage = n % NV;
-      if (n >= NV && !wait_use(sh.vempty[stage], n / NV - 1)) return false;
-      const int s = lane / C::kPanels, pn = lane % C::kPanels;
-      const int row = lane < 4 * C::kPanels ? sh.rows[n % C::kRing][s] : -1;
-      const uint32_t boxes = __popc(__ballot_sync(FULL, row >= 0));
-      if (lane == 0) {
-        if (boxes) mbar_arrive_expect_tx(bar(sh.vfull[stage]), boxes * kSliceTokens * 128);
-        else mbar_arrive(bar(sh.vfull[stage]));
-      }
-      __syncwarp();
-      if (row >= 0)
-        tma_load_2d(v_s + stage * C::kKBytes + pn * C::kKVPanelBytes + s * kSliceTokens * 128, &vmap,
-                    bar(sh.vfull[stage]), pn * 64, row);
-      issued_v = n + 1;
       return true;
     };
     walk.start(p, sh.before, line.start(range), line.start(range + 1), lane);
@@ -460,117 +454,142 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     more = find();
     first = more ? page_of(nxt, lane) : -1;
     ok = advance();
-    // A K stage frees when the S that read it is done, a V stage when its P V is.
-    // P V trails S by LAG tiles, so V(j - NK + NV - LAG) goes out behind K(j).
-    constexpr int BEHIND = NK - NV + LAG;
-    while (ok && (live || issued_v < issued_k) && !*abort_flag) {
-      if (live) ok = issue_k();
-      if (ok && (issued_k - issued_v > BEHIND || (!live && issued_v < issued_k))) ok = issue_v();
+    while (ok && live && !*abort_flag) ok = issue();
+    if (lane == 0) {  // no more tiles; the ring's place is free, as for a tile
+      sh.rows[issued % C::kRing][0] = -2;
+      mbar_arrive(bar(sh.rfull[issued % C::kRing]));
     }
     if (!ok) give_up();
     if (!ok || *abort_flag) {
-      // Before the CTA releases its shared memory: give the last loads of each
+      // Before the CTA releases its shared memory: give the last loads of the
       // ring a bounded time to land (earlier ones have, their stages were reused).
-      for (int j = max(issued_k - NK, 0); j < issued_k; ++j)
+      for (int j = max(issued - NK, 0); j < issued; ++j)
         (void)mbar_wait_bounded(bar(sh.kfull[j % NK]), (j / NK) & 1, kDrainLimitNs);
-      for (int j = max(issued_v - NV, 0); j < issued_v; ++j)
-        (void)mbar_wait_bounded(bar(sh.vfull[j % NV]), (j / NV) & 1, kDrainLimitNs);
+    }
+  } else if (warp == 10) {
+    // ================= TMA loads of V (one elected lane) =================
+    if (umma::elect()) {
+      const int box_rows = 1 << p.log2_box;
+      bool ok = true;
+      int n = 0;
+      for (;; ++n) {
+        const int stage = n % NV, at = n % C::kRing;
+        ok = mbar_wait_bounded(bar(sh.rfull[at]), (n / C::kRing) & 1, kWaitLimitNs);
+        if (!ok || *abort_flag) break;
+        const int4 row = *reinterpret_cast<const int4*>(sh.rows[at]);
+        if (row.x == -2) break;
+        ok = n < NV || mbar_wait_bounded(bar(sh.vempty[stage]), (n / NV - 1) & 1, kWaitLimitNs);
+        if (!ok || *abort_flag) break;
+        const uint32_t full = bar(sh.vfull[stage]), dst = v_s + stage * C::kKBytes;
+        const int good = (row.x >= 0) + (row.y >= 0) + (row.z >= 0) + (row.w >= 0);
+        if (good) mbar_arrive_expect_tx(full, good * C::kPanels * box_rows * 128);
+        else mbar_arrive(full);
+        tree_load_boxes<C::kPanels>(dst, &vmap, full, row.x, row.y, row.z, row.w, box_rows);
+      }
+      if (!ok) {
+        raise_error(PA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (!ok || *abort_flag) {  // as for K
+        for (int j = max(n - NV, 0); j < n; ++j)
+          (void)mbar_wait_bounded(bar(sh.vfull[j % NV]), (j / NV) & 1, kDrainLimitNs);
+      }
     }
   } else if (warp == 8) {
-    // ================= MMA issuer (one elected lane) =================
-    const uint32_t idesc_s = umma::idesc_bf16(kTreeRows, TILE, 0, 0);
-    const uint32_t idesc_o = umma::idesc_bf16(kTreeRows, D, 0, 1);
-    auto s_mma = [&](int x) {  // S = Q K(x)^T into the group's buffer (PAIR: both groups')
-      if (!wait_use(sh.kfull[x % NK], x / NK)) return false;
-      umma::fence_after();
-      if (umma::elect()) {
-        const uint32_t kst = k_s + (x % NK) * C::kKBytes;
+    // ================= MMA issuer (one elected lane, from here to the end) =================
+    if (umma::elect()) {
+      const uint32_t idesc_s = umma::idesc_bf16(kTreeRows, TILE, 0, 0);
+      const uint32_t idesc_o = umma::idesc_bf16(kTreeRows, D, 0, 1);
+      // Descriptors of the first Q, K and V bytes; the others lie (bytes / 16) on.
+      const uint64_t q_desc = umma::desc_sw128(q_s, 16, 1024), k_desc = umma::desc_sw128(k_s, 16, 1024);
+      const uint64_t v_desc = umma::desc_sw128(v_s, C::kKVPanelBytes, 1024);
+      auto wait = [&](const uint64_t& b, int use) { return mbar_wait_bounded(bar(b), use & 1, kWaitLimitNs); };
+      auto s_mma = [&](int x) {  // S = Q K(x)^T into the group's buffer (PAIR: both groups')
+        if (!wait(sh.kfull[x % NK], x / NK)) return false;
+        umma::fence_after();
+        const uint64_t kd = k_desc + (uint32_t)(x % NK) * (C::kKBytes / 16);
         const int k = count_of(x);
 #pragma unroll
         for (int t = 0; t < C::kRowTiles; ++t) {
           const int w = PAIR ? t : group_of(x);
           const uint32_t col = tmem + C::kSCol + (2 * w + (k & 1)) * TILE;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t ad =
-                umma::desc_sw128(q_s + t * C::kQBytes + (kk >> 2) * C::kQPanelBytes + (kk & 3) * 32, 16, 1024);
-            const uint64_t bd = umma::desc_sw128(kst + (kk >> 2) * C::kKVPanelBytes + (kk & 3) * 32, 16, 1024);
-            umma::mma_f16(col, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma::mma_f16(col, q_desc + (t * C::kQBytes + (kk >> 2) * C::kQPanelBytes + (kk & 3) * 32) / 16,
+                          kd + ((kk >> 2) * C::kKVPanelBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0 ? 1u : 0u);
           umma::commit(bar(sh.sfull[w][k & 1]));
         }
         umma::commit(bar(sh.kempty[x % NK]));
-      }
-      __syncwarp();
-      return true;
-    };
-    int begun = 0;  // pieces whose first P V was issued
-    auto o_mma = [&](int x, bool first) {  // O (+)= P V(x), P in the columns of its S buffer
-      const int k = count_of(x);
-      if (first && begun > 0 && !wait_use(sh.ofree, begun - 1)) return false;  // the last piece's O is read
-      if (first) ++begun;
-#pragma unroll
-      for (int t = 0; t < C::kRowTiles; ++t)
-        if (!wait_use(sh.pready[PAIR ? t : group_of(x)][k & 1], k >> 1)) return false;
-      if (*abort_flag || !wait_use(sh.vfull[x % NV], x / NV)) return false;
-      umma::fence_after();
-      if (umma::elect()) {
-        const uint32_t vst = v_s + (x % NV) * C::kKBytes;
+        return true;
+      };
+      int begun = 0;  // pieces whose first P V was issued
+      auto o_mma = [&](int x, bool first) {  // O (+)= P V(x), P in the columns of its S buffer
+        const int k = count_of(x);
+        if (first && begun > 0 && !wait(sh.ofree, begun - 1)) return false;  // the last piece's O is read
+        if (first) ++begun;
+        if (!wait(sh.vfull[x % NV], x / NV)) return false;
+        const uint64_t vd = v_desc + (uint32_t)(x % NV) * (C::kKBytes / 16);
+        const uint32_t acc = first ? 0u : 1u;
 #pragma unroll
         for (int t = 0; t < C::kRowTiles; ++t) {
+          if (!wait(sh.pready[PAIR ? t : group_of(x)][k & 1], k >> 1)) return false;
+          if (PAIR && t == 0 && !wait(sh.pready[1][k & 1], k >> 1)) return false;  // both groups mend V's edge tiles
+          umma::fence_after();
           const int w = PAIR ? t : group_of(x);
           const uint32_t pcol = tmem + C::kSCol + (2 * w + (k & 1)) * TILE;
 #pragma unroll
-          for (int kk = 0; kk < TILE / 16; ++kk) {
-            const uint64_t bd = umma::desc_sw128(vst + kk * 16 * 128, C::kKVPanelBytes, 1024);
-            umma::mma_f16_tmem_a(tmem + C::kOCol + t * D, pcol + kk * 8, bd, idesc_o, (!first || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < TILE / 16; ++kk)
+            umma::mma_f16_tmem_a(tmem + C::kOCol + t * D, pcol + kk * 8, vd + kk * 16 * 128 / 16, idesc_o,
+                                 kk > 0 ? 1u : acc);
           umma::commit(bar(sh.odone[w][k & 1]));
         }
         umma::commit(bar(sh.vempty[x % NV]));
-      }
-      __syncwarp();
-      return true;
-    };
-    // S of a tile goes out before P V of the tile LAG before, except where a
-    // piece starts: its Q takes the place of the last piece's, so its first S
-    // waits for that load, and P V does not wait for it.
-    bool ok = true;
-    uint32_t starts = 0;  // bit j: tile x - 1 - j is the first of its piece
-    int x = 0, q_issued = 0;
-    TreePiece c;
-    for (int u = 0; ok && (ok = piece(u, c)) && c.b >= 0; ++u) {
-      for (int i = c.t0; ok && i < c.t1; ++i, ++x) {
-        const bool first = i == c.t0;
-        auto o_before = [&]() { return x < LAG || o_mma(x - LAG, (starts >> (LAG - 1)) & 1u); };
-        if (first) {
-          ok = x == 0 || wait_use(sh.sfull[PAIR ? 1 : group_of(x - 1)][count_of(x - 1) & 1], count_of(x - 1) >> 1);
-          if (!ok) break;
-          if (umma::elect()) {
+        return true;
+      };
+      // S of a tile goes out before P V of the tile LAG before, except where a
+      // piece starts: its Q takes the place of the last piece's, so its first S
+      // waits for that load, and P V does not wait for it.
+      bool ok = true;
+      uint32_t starts = 0;  // bit j: tile x - 1 - j is the first of its piece
+      int x = 0, u = 0;
+      TreePiece c;
+      for (;; ++u) {
+        ok = wait(sh.pfull[u % kTreePieces], u / kTreePieces);
+        if (!ok || *abort_flag) break;
+        c = sh.pieces[u % kTreePieces];
+        mbar_arrive(bar(sh.pempty[u % kTreePieces]));
+        if (c.b < 0) break;
+        for (int i = c.t0; ok && i < c.t1; ++i, ++x) {
+          const bool first = i == c.t0;
+          auto o_before = [&]() { return x < LAG || o_mma(x - LAG, (starts >> (LAG - 1)) & 1u); };
+          if (first) {
+            ok = x == 0 || wait(sh.sfull[PAIR ? 1 : group_of(x - 1)][count_of(x - 1) & 1], count_of(x - 1) >> 1);
+            if (!ok) break;
             const int tiles = min(C::kRowTiles, p.m_tiles - mt0);
             mbar_arrive_expect_tx(bar(sh.qfull), tiles * C::kPanels * p.q_nodes * G * 128);
             for (int t = 0; t < tiles; ++t)
               for (int k = 0; k < C::kPanels; ++k)
                 tma_load_3d(q_s + t * C::kQBytes + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k * 64, c.g * G,
                             c.b * p.tree_len + (mt0 + t) * p.q_nodes);
-            q_issued = u + 1;
+            ok = o_before() && wait(sh.qfull, u) && s_mma(x);
+          } else {
+            ok = s_mma(x) && o_before();
           }
-          __syncwarp();
-          ok = o_before() && wait_use(sh.qfull, u) && s_mma(x);
-        } else {
-          ok = s_mma(x) && o_before();
+          starts = starts << 1 | (first ? 1u : 0u);
         }
-        starts = starts << 1 | (first ? 1u : 0u);
+        if (!ok || *abort_flag) break;
       }
-    }
-    for (int y = max(x - LAG, 0); ok && y < x; ++y) ok = o_mma(y, (starts >> (x - 1 - y)) & 1u);
-    if (!ok) give_up();
-    if (!ok || *abort_flag) {  // the MMAs and loads issued get a bounded time to finish before TMEM is freed
-      if (umma::elect()) {
+      for (int y = max(x - LAG, 0); ok && !*abort_flag && y < x; ++y) ok = o_mma(y, (starts >> (x - 1 - y)) & 1u);
+      if (!ok) {
+        raise_error(PA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (!ok || *abort_flag) {  // the MMAs and loads issued get a bounded time to finish before TMEM is freed
         umma::commit(bar(sh.drain));
-        if (q_issued > 0) (void)mbar_wait_bounded(bar(sh.qfull), (q_issued - 1) & 1, kDrainLimitNs);
+        if (x > 0 || u > 0) (void)mbar_wait_bounded(bar(sh.qfull), u & 1, kDrainLimitNs);
+        (void)mbar_wait_bounded(bar(sh.qfull), (u + 1) & 1, kDrainLimitNs);
+        (void)mbar_wait_bounded(bar(sh.drain), 0, kDrainLimitNs);
       }
-      (void)mbar_wait_bounded(bar(sh.drain), 0, kDrainLimitNs);
     }
   } else {
     // ================= softmax warps 0-7: one query row per thread =================
@@ -607,7 +626,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     bool ok = true;
     int x0 = 0;  // the CTA's tiles before this piece
     TreePiece c;
-    for (int u = 0; ok && (ok = piece(u, c)) && c.b >= 0; ++u) {
+    for (int u = 0; ok; ++u) {
+      ok = wait_use(sh.pfull[u % kTreePieces], u / kTreePieces);
+      if (!ok) break;
+      c = sh.pieces[u % kTreePieces];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
+      if (c.b < 0) break;
       const TreeSeq s{c.L, c.n, c.L - c.n};
       const int rows = max(0, min(p.q_nodes, c.n - mt * p.q_nodes)) * G;
       const bool real = r < rows, active = 32 * quad < rows;

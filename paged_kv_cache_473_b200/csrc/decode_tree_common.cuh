@@ -33,6 +33,7 @@ struct TreeParams {
   int* queue;                   // ranges claimed, for each CTA of a group (zero between calls)
   int batch, tree_len, hq, hkv, group;
   int block_size, log2_bs, max_blocks, num_blocks;
+  int log2_box;                 // rows of a K/V box: a block's, up to a tile's 64
   int window, max_context;
   int q_nodes, m_tiles;         // nodes per row tile of at most 128 query rows, row tiles of a tree_len tree
   float scale, softcap;

@@ -66,11 +66,12 @@ inline bool tensor_map_encoder() {
 }
 
 // The cache viewed as a 2-D bf16 tensor [rows = num_blocks*Hkv*bs][head_dim];
-// a box is 64 columns (128 B) x 16 rows, landed with 128-byte swizzle.
-inline bool encode_cache_map(CUtensorMap* map, const void* base, int head_dim, long long rows) {
+// a box is 64 columns (128 B) x 16 rows (or box_rows), landed with 128-byte swizzle.
+inline bool encode_cache_map(CUtensorMap* map, const void* base, int head_dim, long long rows,
+                             int box_rows = pa::kSliceTokens) {
   cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)pa::kSliceTokens};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

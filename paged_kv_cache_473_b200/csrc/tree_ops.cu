@@ -143,8 +143,8 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t s
   using Cfg = pa::TreeCfg<D, QR, PAIR>;
   CUtensorMap qmap, kmap, vmap;
   const long long rows = (long long)p.num_blocks * p.hkv * p.block_size;
-  if (!tensor_map_encoder() || !encode_q_map(&qmap, p, D) || !encode_cache_map(&kmap, p.k_cache, D, rows) ||
-      !encode_cache_map(&vmap, p.v_cache, D, rows))
+  if (!tensor_map_encoder() || !encode_q_map(&qmap, p, D) || !encode_cache_map(&kmap, p.k_cache, D, rows, 1 << p.log2_box) ||
+      !encode_cache_map(&vmap, p.v_cache, D, rows, 1 << p.log2_box))
     return cudaErrorInvalidValue;
   auto kern = pa::decode_tree_kernel<D, QR, PAIR>;
   static std::atomic<uint64_t> smem_done{0};
@@ -306,6 +306,7 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   p.group = num_q_heads / num_kv_heads;
   p.block_size = block_size;
   p.log2_bs = ilog2(block_size);
+  p.log2_box = std::min(p.log2_bs, ilog2(pa::kTreeTile));
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.window = window;
