@@ -21,7 +21,8 @@
 //     bound by that: 8 trees of 64 over 16K-128K keys 583 us, every byte
 //     twice from DRAM.)
 //
-// Split.  The tiles of all units, in order, are one line of work.  Its first
+// Split.  The units, in order, are one line of work: of each, a fixed cost (its Q,
+// masks and rows, counted in tiles) and its tiles.  The line's first
 // part is cut into one range for each CTA (of a row tile or pair); the rest into
 // shorter ranges that CTAs claim when they are done, since SMs stream at rates up
 // to a third apart.  A range is a sequence of pieces of units; loads run on into the
@@ -90,6 +91,7 @@ struct TreeCfg {
   static constexpr int kSmemBytes = kBarOff + kSharedBytes;
   static constexpr int kRing = kKStages <= 4 ? 8 : 16;  // tiles whose rows are remembered: those loaded and not done
   static constexpr int kLag = PAIR ? 1 : 2;             // tiles that S runs ahead of P V
+  static constexpr int kUnitCost = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // of a unit, in tiles of this head_dim (about 1.5 us)
   static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
   static constexpr int kSCol = 256;                     // four S buffers, two per group
   static_assert(!PAIR || D <= 128, "tensor memory");
@@ -119,14 +121,16 @@ struct TreeShared {
   uint8_t skip[C::kRing];  // by tile: 16-row slices whose block id is bad
   float m[PAIR ? 1 : 2][PAIR ? 1 : QR];  // running maximum, by tile parity
   float l[PAIR ? 1 : 2][PAIR ? 1 : QR];  // the groups' sums at a piece's end
-  long long before[kTreeWarps + 1];      // tiles before each tenth of the batch
+  long long before[kTreeWarps + 1];      // the line before each warp's part of the batch
+  long long rel0;                        // where the CTA's first range starts: a sequence, and how far in
+  int b0;
   uint32_t tmem;
   int abort;
 };
 
-// The line of work and its ranges: [0, groups) of `per` tiles, then claimed ones of `chunk`.
+// The line of work and its ranges: [0, groups) of `per`, then claimed ones of `chunk`.
 struct TreeLine {
-  long long total, per, chunk, fixed;  // fixed = tiles of the first `groups` ranges
+  long long total, per, chunk, fixed;  // fixed: that of the first `groups` ranges
   int groups, ranges;
 
   __device__ __forceinline__ void cut(long long all, int n) {
@@ -154,6 +158,7 @@ struct TreeLine {
   }
 };
 
+// Tiles of a unit of this sequence.
 __device__ __forceinline__ int tree_unit_tiles(const TreeParams& p, const TreeSeq& s) {
   return s.n > 0 ? (s.L - (tree_start(s, p.window) & ~(kTreeTile - 1)) + kTreeTile - 1) / kTreeTile : 0;
 }
@@ -163,12 +168,16 @@ __device__ __forceinline__ int tree_scan_step(const TreeParams& p) {
   return (p.batch + kTreeThreads - 1) / kTreeThreads;
 }
 
-// Tiles of this lane's sequences in `warp`'s part of the batch, and before them within that part.
-__device__ __forceinline__ long long tree_lane_tiles(const TreeParams& p, int warp, int lane, bool report,
-                                                     long long& before, long long& all) {
+// What this lane's sequences in `warp`'s part of the batch take of the line, and what is before them in that part.
+template <int COST>
+__device__ __forceinline__ long long tree_lane_work(const TreeParams& p, int warp, int lane, bool report,
+                                                    long long& before, long long& all) {
   const int step = tree_scan_step(p), b0 = (warp * 32 + lane) * step;
   long long v = 0;
-  for (int b = b0; b < min(b0 + step, p.batch); ++b) v += (long long)p.hkv * tree_unit_tiles(p, tree_seq(p, b, report));
+  for (int b = b0; b < min(b0 + step, p.batch); ++b) {
+    const int tiles = tree_unit_tiles(p, tree_seq(p, b, report));
+    if (tiles > 0) v += (long long)p.hkv * (tiles + COST);
+  }
   long long incl = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -181,37 +190,41 @@ __device__ __forceinline__ long long tree_lane_tiles(const TreeParams& p, int wa
 }
 
 // Walks the pieces of a range (one warp, the same in all lanes).
+template <int COST>
 struct TreeWalk {
   long long w, w1;
   int b, off, tiles, ulo;
   TreeSeq s;
   int next_len, next_nodes;  // of sequence b + 1, loaded ahead
 
-  // Start at tile `from` of the line, to before `to`; before[i]: tiles before warp part i of the batch.
-  __device__ __forceinline__ void start(const TreeParams& p, const long long* before, long long from, long long to,
-                                        int lane) {
-    constexpr uint32_t FULL = 0xffffffffu;
+  __device__ __forceinline__ int seq_work(const TreeParams& p) const { return tiles > 0 ? p.hkv * (tiles + COST) : 0; }
+
+  // Start at `from` on the line, to before `to`; sequences from b0 on, `rel` after their start, are there.
+  __device__ __forceinline__ void start(const TreeParams& p, long long from, long long to, int b0, long long rel) {
     w = from;
     w1 = to;
-    if (w >= w1) return;
-    const int part = __popc(__ballot_sync(FULL, lane > 0 && lane < kTreeWarps && before[lane] <= from));
-    long long ahead, all;
-    const long long v = tree_lane_tiles(p, part, lane, false, ahead, all);
-    ahead += before[part];
-    const int src = __ffs(__ballot_sync(FULL, v > 0 && from >= ahead && from < ahead + v)) - 1;
-    if (src < 0) {  // cannot be: from < to <= total
-      w = w1;
-      return;
-    }
-    long long rel = from - __shfl_sync(FULL, ahead, src);
-    b = (part * 32 + src) * tree_scan_step(p);
+    b = b0;
     load(p);
-    while (rel >= (long long)p.hkv * tiles && b + 1 < p.batch) {
-      rel -= (long long)p.hkv * tiles;
+    while (rel >= seq_work(p) && b + 1 < p.batch) {
+      rel -= seq_work(p);
       ++b;
       load_next(p);
     }
     off = (int)rel;
+  }
+  // The same, to find where that is; before[i]: the line before warp part i of the batch.
+  __device__ __forceinline__ void find(const TreeParams& p, const long long* before, long long from, long long to,
+                                       int lane) {
+    constexpr uint32_t FULL = 0xffffffffu;
+    w = w1 = to;
+    if (from >= to) return;
+    const int part = __popc(__ballot_sync(FULL, lane > 0 && lane < kTreeWarps && before[lane] <= from));
+    long long ahead, all;
+    const long long v = tree_lane_work<COST>(p, part, lane, false, ahead, all);
+    ahead += before[part];
+    const int src = __ffs(__ballot_sync(FULL, v > 0 && from >= ahead && from < ahead + v)) - 1;
+    if (src < 0) return;  // cannot be: from < to <= total
+    start(p, from, to, (part * 32 + src) * tree_scan_step(p), from - __shfl_sync(FULL, ahead, src));
   }
   __device__ __forceinline__ void fit(const TreeParams& p, int len, int nodes) {
     s = tree_fit(p, len, nodes, false);
@@ -225,23 +238,24 @@ struct TreeWalk {
     fit(p, p.context_lens[b], p.tree_lens ? p.tree_lens[b] : p.tree_len);
   }
   __device__ __forceinline__ void load_next(const TreeParams& p) { fit(p, next_len, next_nodes); }
-  // The next piece that has rows from node `first_node` on; `at`: where its unit starts on the line.
+  // The next piece that has rows from node `first_node` on; `at`: where its unit's tile 0 is on the line.
   __device__ __forceinline__ bool next(const TreeParams& p, int first_node, TreePiece& o, long long& at) {
     while (w < w1) {
-      while (off >= p.hkv * tiles) {  // w < w1 <= total: a sequence with tiles left exists
+      while (off >= seq_work(p)) {  // w < w1 <= total: a sequence with work left exists
         if (b + 1 >= p.batch) return false;
         ++b;
         off = 0;
         load_next(p);
       }
-      o.g = off / tiles;
-      o.t0 = off - o.g * tiles;
-      const int n = (int)min((long long)(tiles - o.t0), w1 - w);
-      o.t1 = o.t0 + n;
-      at = w - o.t0;
+      const int unit = tiles + COST;
+      o.g = off / unit;
+      const int q = off - o.g * unit, n = (int)min((long long)(unit - q), w1 - w);
+      o.t0 = max(q - COST, 0);
+      o.t1 = q + n - COST;
+      at = w - q + COST;
       w += n;
       off += n;
-      if (first_node >= s.n) continue;
+      if (o.t1 <= 0 || first_node >= s.n) continue;  // only of the unit's cost; no rows in these row tiles
       o.b = b;
       o.tiles = tiles;
       o.L = s.L;
@@ -325,11 +339,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid < 12) sh.bad[tid / 4][tid % 4] = 0;
   if (warp == 0) umma::alloc(smem_addr(&sh.tmem), 512);
   pdl_wait();  // a programmatic dependent: nothing of global memory was touched before
-  {
-    long long before, all;
-    tree_lane_tiles(p, warp, lane, blockIdx.x == 0, before, all);
-    if (lane == 0) sh.before[warp + 1] = all;
-  }
+  long long before, all;
+  const long long mine = tree_lane_work<C::kUnitCost>(p, warp, lane, blockIdx.x == 0, before, all);
+  if (lane == 0) sh.before[warp + 1] = all;
   umma::fence_before();
   __syncthreads();
   umma::fence_after();
@@ -340,6 +352,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   TreeLine line;
   line.cut(sh.before[kTreeWarps], gridDim.x / pairs);
+  before += sh.before[warp];
+  const long long from = line.start(grp);
+  if (mine > 0 && from >= before && from < before + mine) {
+    sh.b0 = tid * tree_scan_step(p);
+    sh.rel0 = from - before;
+  }
+  __syncthreads();
   const uint32_t tmem = sh.tmem;
   const uint32_t s_base = smem_addr(smem);
   const uint32_t q_s = s_base + C::kQOff, k_s = s_base + C::kKOff, v_s = s_base + C::kVOff;
@@ -362,7 +381,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // wb + l (pages) and wb + 32 + l (pages2); the next piece, and the block ids
     // of its first window, are looked up a piece ahead, so that no load waits
     // for a length or a block table.
-    TreeWalk walk;
+    TreeWalk<C::kUnitCost> walk;
     TreePiece cur, nxt;
     int range = grp, u = 0, i = 0, wb = 0, pages = -1, pages2 = -1, first = -1;
     bool more = true, live = true, ok = true;
@@ -390,7 +409,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) claim = atomicAdd(p.queue + pair, 1);
         range = line.groups + __shfl_sync(FULL, claim, 0);
         if (range >= line.ranges) return false;
-        walk.start(p, sh.before, line.start(range), line.start(range + 1), lane);
+        walk.find(p, sh.before, line.start(range), line.start(range + 1), lane);
       }
     };
     auto advance = [&]() {  // to the next piece, which goes into the ring
@@ -449,7 +468,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (++i >= cur.t1) return advance();
       return true;
     };
-    walk.start(p, sh.before, line.start(range), line.start(range + 1), lane);
+    walk.w = walk.w1 = 0;
+    if (line.start(range) < line.start(range + 1))
+      walk.start(p, line.start(range), line.start(range + 1), sh.b0, sh.rel0);
     if (blockIdx.x == 0 && lane == 0) p.ws_rec[-1].x = line.ranges;  // how many records there are
     more = find();
     first = more ? page_of(nxt, lane) : -1;
@@ -548,7 +569,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       };
       // S of a tile goes out before P V of the tile LAG before, except where a
       // piece starts: its Q takes the place of the last piece's, so its first S
-      // waits for that load, and P V does not wait for it.
+      // waits for that load, and the last piece's P V, which its rows wait for,
+      // go first.
       bool ok = true;
       uint32_t starts = 0;  // bit j: tile x - 1 - j is the first of its piece
       int x = 0, u = 0;
@@ -572,6 +594,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tma_load_3d(q_s + t * C::kQBytes + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k * 64, c.g * G,
                             c.b * p.tree_len + (mt0 + t) * p.q_nodes);
             ok = o_before() && wait(sh.qfull, u) && s_mma(x);
+          } else if (i < c.t0 + LAG) {
+            ok = o_before() && s_mma(x);
           } else {
             ok = s_mma(x) && o_before();
           }
@@ -625,22 +649,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     bool ok = true;
     int x0 = 0;  // the CTA's tiles before this piece
-    TreePiece c;
-    for (int u = 0; ok; ++u) {
-      ok = wait_use(sh.pfull[u % kTreePieces], u / kTreePieces);
-      if (!ok) break;
-      c = sh.pieces[u % kTreePieces];
+    TreePiece c, nxt;
+    TreeRow row, row_nxt;
+    auto take = [&](int u) {  // piece u, which is in the ring, and what this row attends in it
+      nxt = sh.pieces[u % kTreePieces];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
+      row_nxt = TreeRow{0, 0};
+      if (nxt.b >= 0) row_nxt = tree_row(p, TreeSeq{nxt.L, nxt.n, nxt.L - nxt.n}, nxt.b, node);
+    };
+    bool taken = false;
+    for (int u = 0; ok; ++u) {
+      if (!taken) {
+        ok = wait_use(sh.pfull[u % kTreePieces], u / kTreePieces);
+        if (!ok) break;
+        take(u);
+      }
+      taken = false;
+      c = nxt;
+      row = row_nxt;
       if (c.b < 0) break;
-      const TreeSeq s{c.L, c.n, c.L - c.n};
       const int rows = max(0, min(p.q_nodes, c.n - mt * p.q_nodes)) * G;
       const bool real = r < rows, active = 32 * quad < rows;
-      const int L = c.L, base = s.base, kt0 = c.ulo & ~(TILE - 1), len = c.t1 - c.t0;
-      TreeRow row;
-      row.lo = base;
-      row.nodes = 0;
-      if (real) row = tree_row(p, s, c.b, node);
+      const int L = c.L, base = L - c.n, kt0 = c.ulo & ~(TILE - 1), len = c.t1 - c.t0;
       // Rows' windows start in [ulo, ulo + 63] (a depth is at most 63) and at most at base.
       const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;
       uint64_t* bad = sh.bad[u % 3];
@@ -656,6 +687,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool masked = edge || kt < c.ulo || skip != 0;
         const uint32_t s_col = lane_base + C::kSCol + (2 * grp_w + (k & 1)) * TILE;
         if (active) {
+          if (pre || masked) {
+            // Cap and masks, in place and 16 columns at a time: this path is
+            // rare or bound by its exponentials, and unrolled over the tile it
+            // was most of the kernel's code (its first pass, from a cold
+            // instruction cache, took 11,000 cycles).
+            uint64_t see = ~0ull;
+            if (masked) {  // bit e: this row attends position kt + e
+              const int from = min(max(row.lo - kt, 0), TILE), to = min(max(base - kt, 0), TILE);
+              see = low_bits(to) & ~low_bits(from);
+              if (kt >= base) see |= row.nodes >> (kt - base);
+              else if (base - kt < TILE) see |= row.nodes << (base - kt);
+              for (int e = 0; e < 4; ++e)
+                if ((skip >> e) & 1u) see &= ~(0xffffull << (16 * e));
+            }
+#pragma unroll 1
+            for (int e = 0; e < TILE; e += 16) {
+              float v[16];
+              umma::ld16(s_col + e, v);
+              if (p.use_softcap) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  float a, q;
+                  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(v[j] * cap_c));
+                  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + a));
+                  v[j] = fmaf(-cap_b, q, cap_a);
+                }
+              } else if (pre) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] *= xs_all;
+              }
+              const uint32_t bits = (uint32_t)(see >> e);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = (bits >> j) & 1u ? v[j] : -CUDART_INF_F;
+              umma::st16(s_col + e, v);
+            }
+          }
           float y[TILE];
           {
             uint32_t v[TILE / 16][16];
@@ -665,40 +732,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int e = 0; e < TILE; ++e) y[e] = __uint_as_float(v[e / 16][e % 16]);
           }
-          if (pre) {
-            if (p.use_softcap) {
-#pragma unroll
-              for (int e = 0; e < TILE; ++e) {
-                float a, q;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(y[e] * cap_c));
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + a));
-                y[e] = fmaf(-cap_b, q, cap_a);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < TILE; ++e) y[e] *= xs_all;
-            }
-          }
-          if (masked) {
-            // Bit e: this row attends position kt + e.
-            const int from = min(max(row.lo - kt, 0), TILE), to = min(max(base - kt, 0), TILE);
-            uint64_t see = low_bits(to) & ~low_bits(from);
-            if (kt >= base) see |= row.nodes >> (kt - base);
-            else if (base - kt < TILE) see |= row.nodes << (base - kt);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((skip >> e) & 1u) see &= ~(0xffffull << (16 * e));
-            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
-#pragma unroll
-            for (int e = 0; e < TILE; ++e) y[e] = ((e < 32 ? lo >> e : hi >> (e - 32)) & 1u) ? y[e] : -CUDART_INF_F;
-          }
           float mx[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mx[e] = y[e];
+          for (int e = 0; e < 8; ++e) mx[e] = max3(y[e], y[e + 8], y[e + 16]);
 #pragma unroll
-          for (int e = 8; e < TILE; ++e) mx[e & 7] = fmaxf(mx[e & 7], y[e]);
-          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * xs;  // xs > 0
+          for (int e = 24; e < 56; e += 16)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mx[j] = max3(mx[j], y[e + j], y[e + 8 + j]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx[j] = fmaxf(mx[j], y[56 + j]);
+          const float top = fmaxf(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7])) * xs;  // xs > 0
           // The reference so far: this group's, or (not PAIR) the tile's before, the other group's.
           float before = m;
           if (!PAIR) {
@@ -724,17 +767,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // Weights in fp32 for the sum, rounded to bf16 for the second product
           // (a relative 2^-8 at most on each weight, what the output's own
           // rounding allows; the tensor cores take both operands in one type).
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 xs2 = make_float2(xs, xs), ref2 = make_float2(-ref, -ref);
           uint32_t pk[TILE / 2];
 #pragma unroll
           for (int e = 0; e < TILE / 2; ++e) {
-            float e0, e1;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fmaf(y[2 * e], xs, -ref)));
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fmaf(y[2 * e + 1], xs, -ref)));
-            ps[e & 3] += e0 + e1;
-            pk[e] = pack_bf16x2(e0, e1);
+            const float2 a = fma_f32x2(make_float2(y[2 * e], y[2 * e + 1]), xs2, ref2);
+            float2 w;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(a.x));
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(a.y));
+            ps[e & 1] = add_f32x2(ps[e & 1], w);
+            pk[e] = pack_bf16x2(w.x, w.y);
           }
-          l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+          l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
           umma::st16_nowait(s_col, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
           umma::st16_nowait(s_col + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
           // (The first tile's P V overwrites O; rows that nobody reads move nothing.)
@@ -769,36 +814,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             return vst + (rem >> 3) * C::kKVPanelBytes + e * 128 + ((rem & 7) << 4);
           };
           // Rows of V that no row attends: zero (they were not loaded, or hold what stands behind the end).
-          uint64_t none = low_bits(min(max(c.ulo - kt, 0), TILE)) | ~low_bits(min(max(L - kt, 0), TILE));
-#pragma unroll
+          auto clear = [&](int from, int to) {
+            for (int idx = from * CPR + me; idx < to * CPR; idx += NT)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(idx)), "r"(0u) : "memory");
+          };
+          clear(0, min(c.ulo - kt, TILE));
+          clear(max(L - kt, 0), TILE);
           for (int e = 0; e < 4; ++e)
-            if ((skip >> e) & 1u) none |= 0xffffull << (16 * e);
-          if (none) {
-            for (int idx = me; idx < TILE * CPR; idx += NT)
-              if ((none >> (idx / CPR)) & 1ull)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(idx)), "r"(0u) : "memory");
-          }
+            if ((skip >> e) & 1u) clear(16 * e, 16 * e + 16);
           if (edge) {
-            const int slot = kt + TILE > base ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - kt0) / TILE;
-            constexpr int U = TILE * CPR / NT < 4 ? TILE * CPR / NT : 4;
+            // Rows that some may attend and some not: the tree's, those at the windows' starts.
+            const bool tree = kt + TILE > base, starts = kt < w_end;
+            const int slot = tree ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - kt0) / TILE;
+            const int end = (tree ? min(L - kt, TILE) : min(w_end - kt, TILE)) * CPR;
+            constexpr int U = 4;
 #pragma unroll 1
-            for (int i0 = me; i0 < TILE * CPR; i0 += NT * U) {
+            for (int i0 = max(starts ? c.ulo - kt : base - kt, 0) * CPR + me; i0 < end; i0 += NT * U) {
               uint32_t v[U][4], exps = 0;
 #pragma unroll
-              for (int e = 0; e < U; ++e)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[e][0]), "=r"(v[e][1]), "=r"(v[e][2]), "=r"(v[e][3])
-                             : "r"(chunk(i0 + NT * e)));
+              for (int e = 0; e < U; ++e) {
+                v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0;
+                if (i0 + NT * e < end)
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(v[e][0]), "=r"(v[e][1]), "=r"(v[e][2]), "=r"(v[e][3])
+                               : "r"(chunk(i0 + NT * e)));
+              }
 #pragma unroll
               for (int e = 0; e < U; ++e)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) exps = __vmaxu2(exps, v[e][j] & 0x7f807f80u);
-              // Exponent bits all set in some element: not finite.  (Rows just
-              // zeroed by another thread may still read as what stood there.)
+              // Exponent bits all set in some element: not finite.
               if ((exps & 0xffffu) != 0x7f80u && (exps >> 16) != 0x7f80u) continue;
               for (int e = 0; e < U; ++e) {
                 const int idx = i0 + NT * e, at = idx / CPR;
-                if ((none >> at) & 1ull) continue;
+                if (idx >= end || ((skip >> (at >> 4)) & 1u)) continue;
                 bool found = false;
                 for (int j = 0; j < 4; ++j) {
                   if ((v[e][j] & 0x7f80u) == 0x7f80u) v[e][j] &= 0xffff0000u, found = true;
@@ -819,6 +868,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) mbar_arrive(bar(sh.pready[grp_w][k & 1]));
       }
       if (!ok || *abort_flag) break;
+
+      // The next piece, if it is known already: its masks come while this one's last P V runs.
+      taken = __all_sync(FULL, mbar_try_wait(bar(sh.pfull[(u + 1) % kTreePieces]), ((u + 1) / kTreePieces) & 1));
+      if (taken) take(u + 1);
 
       // ---- write the piece's rows -------------------------------------------------------
       const int last = x0 + len - 1, kl = count_of(last);
@@ -853,13 +906,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             ((int64_t)c.b * p.tree_len * p.hq + (int64_t)c.g * G + head) * D;
       if (active) {
         // Not PAIR: each group writes half of the columns.
-        const int e0 = PAIR ? 0 : grp_w * (D / 32), e1 = PAIR ? D / 16 : e0 + D / 32;
-#pragma unroll 2
-        for (int e = e0; e < e1; ++e) {
-          float v[16];
-          umma::ld16(o_col + e * 16, v);
-          if (marks && real) {  // give back what was taken out of V, to a row that attends it
-            for (int z = 0; z < 4; ++z) {
+        constexpr int CH = PAIR ? D / 16 : D / 32, U = CH < 4 ? CH : 4;  // 16-column chunks, in flight
+        const int e0 = PAIR ? 0 : grp_w * CH;
+        if (marks) {  // give back what was taken out of V, to the rows that attend it
+#pragma unroll 1
+          for (int e = e0; e < e0 + CH; ++e) {
+            float v[16];
+            umma::ld16(o_col + e * 16, v);
+            for (int z = 0; real && z < 4; ++z) {
               uint64_t rest = bad[z];
               const int kt = z < 2 ? kt0 + z * TILE : (base & ~(TILE - 1)) + (z - 2) * TILE;
               while (rest) {
@@ -876,23 +930,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
               }
             }
+            __syncwarp();
+            umma::st16(o_col + e * 16, v);
           }
+        }
+#pragma unroll 1
+        for (int e = e0; e < e0 + CH; e += U) {
+          uint32_t v[U][16];
+#pragma unroll
+          for (int z = 0; z < U; ++z) umma::ld16_nowait(o_col + (e + z) * 16, v[z]);
+          umma::wait_ld();
           if (!real) continue;
-          if (whole) {
-            uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
-            if (sectors) {
-              st_global_32(orow + e * 16, o);
+          for (int z = 0; z < U; ++z) {
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[z][j]);
+            if (whole) {
+              uint32_t o[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f[2 * j] * inv, f[2 * j + 1] * inv);
+              if (sectors) {
+                st_global_32(orow + (e + z) * 16, o);
+              } else {
+                reinterpret_cast<uint4*>(orow + (e + z) * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<uint4*>(orow + (e + z) * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+              }
             } else {
-              reinterpret_cast<uint4*>(orow + e * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-              reinterpret_cast<uint4*>(orow + e * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-          } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float4*>(po + (int64_t)(e * 4 + j) * row_stride * 4) =
-                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4*>(po + (int64_t)((e + z) * 4 + j) * row_stride * 4) =
+                    make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            }
           }
         }
         if (real && !whole && (PAIR || grp_w == 0))

@@ -282,7 +282,7 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
   if (tree_len > pa::kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
   if (mask_stride != 0 && mask_stride < tree_len) return PA_ERR_INVALID;
   const long long longest = std::min<long long>(max_context_len, (long long)max_blocks_per_seq * block_size);
-  if ((longest / pa::kTreeTile + 1) * num_kv_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  if ((longest / pa::kTreeTile + 8) * num_kv_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;  // a sequence's work in 32 bits
   if (batch == 0) return PA_OK;
   if (!tree_mask || !aligned(tree_mask, 8) || !aligned(tree_lens, 4)) return PA_ERR_INVALID;
   const bool tensor_cores = dtype == PA_BF16;
