@@ -90,7 +90,7 @@ struct TreeCfg {
   static constexpr int kBarOff = kVOff + kVStages * kKBytes;
   static constexpr int kSmemBytes = kBarOff + kSharedBytes;
   static constexpr int kRing = kKStages <= 4 ? 8 : 16;  // tiles whose rows are remembered: those loaded and not done
-  static constexpr int kLag = PAIR ? 1 : 2;             // tiles that S runs ahead of P V
+  static constexpr int kLag = PAIR ? 2 : 3;             // tiles that S runs ahead of P V
   static constexpr int kUnitCost = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // of a unit, in tiles of this head_dim (about 1.5 us)
   static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
   static constexpr int kSCol = 256;                     // four S buffers, two per group
@@ -384,8 +384,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     TreeWalk<C::kUnitCost> walk;
     TreePiece cur, nxt;
     int range = grp, u = 0, i = 0, wb = 0, pages = -1, pages2 = -1, first = -1;
-    bool more = true, live = true, ok = true;
+    bool more = false, ok = true;
     int4 rec = make_int4(0, 0, 0, 0);  // the unit that starts in this range and goes on: pieces, b, g, nodes
+    cur.t1 = 0;
     auto page_of = [&](const TreePiece& c, int q) {
       const int kt0 = c.ulo & ~(TILE - 1), t = kt0 + c.t0 * TILE + (q << p.log2_box);
       return t < min(c.L, kt0 + c.t1 * TILE) ? p.block_tables[(int64_t)c.b * p.max_blocks + (t >> p.log2_bs)] : -1;
@@ -412,31 +413,43 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         walk.find(p, sh.before, line.start(range), line.start(range + 1), lane);
       }
     };
-    auto advance = [&]() {  // to the next piece, which goes into the ring
-      if (u >= kTreePieces && !wait_use(sh.pempty[u % kTreePieces], u / kTreePieces - 1)) return false;
-      live = more;
-      cur = nxt;
-      if (lane == 0) {
-        if (!live) cur.b = -1;
-        sh.pieces[u % kTreePieces] = cur;
-        mbar_arrive(bar(sh.pfull[u % kTreePieces]));
-      }
-      __syncwarp();
-      ++u;
-      if (!live) return true;
-      i = cur.t0;
-      wb = 0;
-      pages = first;
-      pages2 = page_of(cur, 32 + lane);
-      more = find();
-      first = more ? page_of(nxt, lane) : -1;
-      return true;
-    };
     const int boxes = TILE >> p.log2_box, box_rows = 1 << p.log2_box;  // of a tile: 4, 2 or 1
     int issued = 0;
-    auto issue = [&]() {  // the cursor's tile, as tile number `issued`
+    walk.w = walk.w1 = 0;
+    if (line.start(range) < line.start(range + 1))
+      walk.start(p, line.start(range), line.start(range + 1), sh.b0, sh.rel0);
+    if (blockIdx.x == 0 && lane == 0) p.ws_rec[-1].x = line.ranges;  // how many records there are
+    while (!*abort_flag) {
+      if (i >= cur.t1) {  // the next piece goes into the ring, and the one after it is looked up (at first: both)
+        bool stop = false;
+#pragma unroll 1
+        for (int z = issued > 0 ? 1 : 0; z < 2; ++z) {
+          if (z == 1) {
+            ok = u < kTreePieces || wait_use(sh.pempty[u % kTreePieces], u / kTreePieces - 1);
+            stop = !ok || !more;
+            cur = nxt;
+            if (!more) cur.b = -1;
+            if (ok && lane == 0) {
+              sh.pieces[u % kTreePieces] = cur;
+              mbar_arrive(bar(sh.pfull[u % kTreePieces]));
+            }
+            __syncwarp();
+            ++u;
+            if (stop) break;
+            i = cur.t0;
+            wb = 0;
+            pages = first;
+            pages2 = page_of(cur, 32 + lane);
+          }
+          more = find();
+          first = more ? page_of(nxt, lane) : -1;
+        }
+        if (stop) break;
+      }
+      // The cursor's tile, as tile number `issued`.
       const int n = issued, stage = n % NK, at = n % C::kRing;
-      if (n >= NK && !wait_use(sh.kempty[stage], n / NK - 1)) return false;
+      ok = n < NK || wait_use(sh.kempty[stage], n / NK - 1);
+      if (!ok) break;
       const int rel = boxes * (i - cur.t0);
       if (rel >= wb + 32) {
         wb += 32;
@@ -465,17 +478,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.rfull[at]));
       issued = n + 1;
-      if (++i >= cur.t1) return advance();
-      return true;
-    };
-    walk.w = walk.w1 = 0;
-    if (line.start(range) < line.start(range + 1))
-      walk.start(p, line.start(range), line.start(range + 1), sh.b0, sh.rel0);
-    if (blockIdx.x == 0 && lane == 0) p.ws_rec[-1].x = line.ranges;  // how many records there are
-    more = find();
-    first = more ? page_of(nxt, lane) : -1;
-    ok = advance();
-    while (ok && live && !*abort_flag) ok = issue();
+      ++i;
+    }
     if (lane == 0) {  // no more tiles; the ring's place is free, as for a tile
       sh.rows[issued % C::kRing][0] = -2;
       mbar_arrive(bar(sh.rfull[issued % C::kRing]));
@@ -518,100 +522,108 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else if (warp == 8) {
     // ================= MMA issuer (one elected lane, from here to the end) =================
+    // Everything this lane does between two products delays the next one, so
+    // stages and parities are counted up, not divided out of a tile's number.
     if (umma::elect()) {
       const uint32_t idesc_s = umma::idesc_bf16(kTreeRows, TILE, 0, 0);
       const uint32_t idesc_o = umma::idesc_bf16(kTreeRows, D, 0, 1);
       // Descriptors of the first Q, K and V bytes; the others lie (bytes / 16) on.
       const uint64_t q_desc = umma::desc_sw128(q_s, 16, 1024), k_desc = umma::desc_sw128(k_s, 16, 1024);
       const uint64_t v_desc = umma::desc_sw128(v_s, C::kKVPanelBytes, 1024);
-      auto wait = [&](const uint64_t& b, int use) { return mbar_wait_bounded(bar(b), use & 1, kWaitLimitNs); };
-      auto s_mma = [&](int x) {  // S = Q K(x)^T into the group's buffer (PAIR: both groups')
-        if (!wait(sh.kfull[x % NK], x / NK)) return false;
-        umma::fence_after();
-        const uint64_t kd = k_desc + (uint32_t)(x % NK) * (C::kKBytes / 16);
-        const int k = count_of(x);
-#pragma unroll
-        for (int t = 0; t < C::kRowTiles; ++t) {
-          const int w = PAIR ? t : group_of(x);
-          const uint32_t col = tmem + C::kSCol + (2 * w + (k & 1)) * TILE;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma::mma_f16(col, q_desc + (t * C::kQBytes + (kk >> 2) * C::kQPanelBytes + (kk & 3) * 32) / 16,
-                          kd + ((kk >> 2) * C::kKVPanelBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0 ? 1u : 0u);
-          umma::commit(bar(sh.sfull[w][k & 1]));
-        }
-        umma::commit(bar(sh.kempty[x % NK]));
-        return true;
-      };
-      int begun = 0;  // pieces whose first P V was issued
-      auto o_mma = [&](int x, bool first) {  // O (+)= P V(x), P in the columns of its S buffer
-        const int k = count_of(x);
-        if (first && begun > 0 && !wait(sh.ofree, begun - 1)) return false;  // the last piece's O is read
-        if (first) ++begun;
-        if (!wait(sh.vfull[x % NV], x / NV)) return false;
-        const uint64_t vd = v_desc + (uint32_t)(x % NV) * (C::kKBytes / 16);
-        const uint32_t acc = first ? 0u : 1u;
-#pragma unroll
-        for (int t = 0; t < C::kRowTiles; ++t) {
-          if (!wait(sh.pready[PAIR ? t : group_of(x)][k & 1], k >> 1)) return false;
-          if (PAIR && t == 0 && !wait(sh.pready[1][k & 1], k >> 1)) return false;  // both groups mend V's edge tiles
-          umma::fence_after();
-          const int w = PAIR ? t : group_of(x);
-          const uint32_t pcol = tmem + C::kSCol + (2 * w + (k & 1)) * TILE;
-#pragma unroll
-          for (int kk = 0; kk < TILE / 16; ++kk)
-            umma::mma_f16_tmem_a(tmem + C::kOCol + t * D, pcol + kk * 8, vd + kk * 16 * 128 / 16, idesc_o,
-                                 kk > 0 ? 1u : acc);
-          umma::commit(bar(sh.odone[w][k & 1]));
-        }
-        umma::commit(bar(sh.vempty[x % NV]));
-        return true;
-      };
-      // S of a tile goes out before P V of the tile LAG before, except where a
-      // piece starts: its Q takes the place of the last piece's, so its first S
-      // waits for that load, and the last piece's P V, which its rows wait for,
-      // go first.
+      const uint32_t kfull = bar(sh.kfull[0]), kempty = bar(sh.kempty[0]), vfull = bar(sh.vfull[0]);
+      const uint32_t vempty = bar(sh.vempty[0]), sfull = bar(sh.sfull[0][0]), pready = bar(sh.pready[0][0]);
+      const uint32_t odone = bar(sh.odone[0][0]);
+      auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, kWaitLimitNs); };
+      // S buffer (and its barriers) of tile x for row tile t, and its use's parity.
+      auto buffer = [&](int x, int t) { return PAIR ? 2 * t + (x & 1) : 2 * (x & 1) + (x >> 1 & 1); };
+      auto parity = [&](int x) { return (uint32_t)(PAIR ? x >> 1 : x >> 2) & 1u; };
+      int x = 0, y = 0;                           // next tile of S, of P V
+      uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // their stages, and the parities of these
+      int asked = 0;                              // pieces whose Q load is issued
+      TreePiece next;
+      // Take piece number `asked` from the ring and load its Q.  The last piece's
+      // last S is done, or not issued; false: not in the ring (yet), unless `block`.
       bool ok = true;
-      uint32_t starts = 0;  // bit j: tile x - 1 - j is the first of its piece
-      int x = 0, u = 0;
-      TreePiece c;
-      for (;; ++u) {
-        ok = wait(sh.pfull[u % kTreePieces], u / kTreePieces);
-        if (!ok || *abort_flag) break;
-        c = sh.pieces[u % kTreePieces];
-        mbar_arrive(bar(sh.pempty[u % kTreePieces]));
-        if (c.b < 0) break;
-        for (int i = c.t0; ok && i < c.t1; ++i, ++x) {
-          const bool first = i == c.t0;
-          auto o_before = [&]() { return x < LAG || o_mma(x - LAG, (starts >> (LAG - 1)) & 1u); };
-          if (first) {
-            ok = x == 0 || wait(sh.sfull[PAIR ? 1 : group_of(x - 1)][count_of(x - 1) & 1], count_of(x - 1) >> 1);
-            if (!ok) break;
-            const int tiles = min(C::kRowTiles, p.m_tiles - mt0);
-            mbar_arrive_expect_tx(bar(sh.qfull), tiles * C::kPanels * p.q_nodes * G * 128);
-            for (int t = 0; t < tiles; ++t)
-              for (int k = 0; k < C::kPanels; ++k)
-                tma_load_3d(q_s + t * C::kQBytes + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k * 64, c.g * G,
-                            c.b * p.tree_len + (mt0 + t) * p.q_nodes);
-            ok = o_before() && wait(sh.qfull, u) && s_mma(x);
-          } else if (i < c.t0 + LAG) {
-            ok = o_before() && s_mma(x);
-          } else {
-            ok = s_mma(x) && o_before();
+      auto ask = [&](bool block) {
+        const uint32_t in = bar(sh.pfull[asked % kTreePieces]), par = (asked / kTreePieces) & 1;
+        if (block ? !wait(in, par) : !mbar_try_wait(in, par)) return false;
+        if (x > 0 && !wait(sfull + 8 * buffer(x - 1, PAIR ? 1 : 0), parity(x - 1))) return false;
+        next = sh.pieces[asked % kTreePieces];
+        mbar_arrive(bar(sh.pempty[asked % kTreePieces]));
+        ++asked;
+        if (next.b < 0) return true;
+        const int tiles = min(C::kRowTiles, p.m_tiles - mt0);
+        mbar_arrive_expect_tx(bar(sh.qfull), tiles * C::kPanels * p.q_nodes * G * 128);
+#pragma unroll 1
+        for (int k = 0; k < tiles * C::kPanels; ++k)
+          tma_load_3d(q_s + k * C::kQPanelBytes, &qmap, bar(sh.qfull), k % C::kPanels * 64, next.g * G,
+                      next.b * p.tree_len + (mt0 + k / C::kPanels) * p.q_nodes);
+        return true;
+      };
+      for (int u = 0;; ++u) {
+        ok = asked > u || ask(true);
+        if (!ok || next.b < 0 || *abort_flag) break;
+        // Step i: P V of the piece's tile i - LAG, then S of its tile i, whose buffer
+        // is free by then.  (PAIR: row tile by row tile, so that the second
+        // group's S comes when the first group has finished a tile: the groups, whose
+        // warps share the special function units, run half a tile apart.)  The
+        // last steps have no S: there the next piece's Q is asked for.
+        const int len = next.t1 - next.t0;
+#pragma unroll 1
+        for (int i = 0; ok && i < len + LAG; ++i) {
+          const bool s = i < len, o = i >= LAG;
+          if (o) {
+            if (i == LAG && u > 0) ok = wait(bar(sh.ofree), (u - 1) & 1);  // the last piece's O is read
+            ok = ok && wait(vfull + 8 * vst, vph);
           }
-          starts = starts << 1 | (first ? 1u : 0u);
+          if (s) ok = ok && (i > 0 || wait(bar(sh.qfull), u & 1)) && wait(kfull + 8 * kst, kph);
+          else if (asked == u + 1) (void)ask(false);
+          if (!ok) break;
+#pragma unroll
+          for (int t = 0; t < C::kRowTiles; ++t) {
+            if (o) {
+              const uint32_t at = buffer(y, t);
+              if (!(ok = wait(pready + 8 * at, parity(y)))) break;
+              umma::fence_after();
+              const uint64_t vd = v_desc + vst * (C::kKBytes / 16);
+              const uint32_t pcol = tmem + C::kSCol + at * TILE;
+#pragma unroll
+              for (int kk = 0; kk < TILE / 16; ++kk)
+                umma::mma_f16_tmem_a(tmem + C::kOCol + t * D, pcol + kk * 8, vd + kk * 16 * 128 / 16, idesc_o,
+                                     kk > 0 || i > LAG ? 1u : 0u);
+              umma::commit(odone + 8 * at);
+              if (t == C::kRowTiles - 1) umma::commit(vempty + 8 * vst);
+            }
+            if (s) {
+              umma::fence_after();
+              const uint32_t at = buffer(x, t), col = tmem + C::kSCol + at * TILE;
+              const uint64_t qd = q_desc + t * (C::kQBytes / 16), kd = k_desc + kst * (C::kKBytes / 16);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma::mma_f16(col, qd + ((kk >> 2) * C::kQPanelBytes + (kk & 3) * 32) / 16,
+                              kd + ((kk >> 2) * C::kKVPanelBytes + (kk & 3) * 32) / 16, idesc_s, kk > 0 ? 1u : 0u);
+              umma::commit(sfull + 8 * at);
+              if (t == C::kRowTiles - 1) umma::commit(kempty + 8 * kst);
+            }
+          }
+          if (o) {
+            ++y;
+            if (++vst == NV) vst = 0, vph ^= 1;
+          }
+          if (s) {
+            ++x;
+            if (++kst == NK) kst = 0, kph ^= 1;
+          }
         }
-        if (!ok || *abort_flag) break;
+        if (!ok) break;
       }
-      for (int y = max(x - LAG, 0); ok && !*abort_flag && y < x; ++y) ok = o_mma(y, (starts >> (x - 1 - y)) & 1u);
       if (!ok) {
         raise_error(PA_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
       if (!ok || *abort_flag) {  // the MMAs and loads issued get a bounded time to finish before TMEM is freed
         umma::commit(bar(sh.drain));
-        if (x > 0 || u > 0) (void)mbar_wait_bounded(bar(sh.qfull), u & 1, kDrainLimitNs);
-        (void)mbar_wait_bounded(bar(sh.qfull), (u + 1) & 1, kDrainLimitNs);
+        if (asked > 0) (void)mbar_wait_bounded(bar(sh.qfull), (asked - 1) & 1, kDrainLimitNs);
         (void)mbar_wait_bounded(bar(sh.drain), 0, kDrainLimitNs);
       }
     }
@@ -632,6 +644,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const float xs = pre ? 1.f : xs_all;
     const float cap_a = p.softcap * kLog2e, cap_b = 2.f * cap_a;
     const float cap_c = p.use_softcap ? 2.f * xs_all / p.softcap : 0.f;
+    // Where a score is at most half of the cap, y = s / cap <= 0.5, the Taylor series
+    // y - y^3 / 3 + 2 y^5 / 15 - ... to y^11 is within 5e-7 of tanh y, and takes
+    // the place of two special function results by five packed operations.
+    const float cap_y = p.use_softcap ? p.scale / p.softcap : 0.f;
+    const float cap_lim = p.use_softcap ? 0.5f / fabsf(cap_y) : 0.f;
+    const float2 cap_y2 = make_float2(cap_y, cap_y), cap_s2 = make_float2(xs_all, xs_all);
 
     // Rows of nodes that a tree does not have: no piece writes them.
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
@@ -651,30 +669,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     int x0 = 0;  // the CTA's tiles before this piece
     TreePiece c, nxt;
     TreeRow row, row_nxt;
-    auto take = [&](int u) {  // piece u, which is in the ring, and what this row attends in it
-      nxt = sh.pieces[u % kTreePieces];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
-      row_nxt = TreeRow{0, 0};
-      if (nxt.b >= 0) row_nxt = tree_row(p, TreeSeq{nxt.L, nxt.n, nxt.L - nxt.n}, nxt.b, node);
-    };
-    bool taken = false;
+    nxt.b = -1;
+    // Turn u: the tiles of piece u - 1, the next piece's masks (they come while the
+    // last P V runs), then the rows of piece u - 1.
     for (int u = 0; ok; ++u) {
-      if (!taken) {
-        ok = wait_use(sh.pfull[u % kTreePieces], u / kTreePieces);
-        if (!ok) break;
-        take(u);
-      }
-      taken = false;
       c = nxt;
       row = row_nxt;
-      if (c.b < 0) break;
+      const bool work = u > 0;
       const int rows = max(0, min(p.q_nodes, c.n - mt * p.q_nodes)) * G;
       const bool real = r < rows, active = 32 * quad < rows;
-      const int L = c.L, base = L - c.n, kt0 = c.ulo & ~(TILE - 1), len = c.t1 - c.t0;
+      const int L = c.L, base = L - c.n, kt0 = c.ulo & ~(TILE - 1), len = work ? c.t1 - c.t0 : 0;
       // Rows' windows start in [ulo, ulo + 63] (a depth is at most 63) and at most at base.
       const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;
-      uint64_t* bad = sh.bad[u % 3];
+      uint64_t* bad = sh.bad[(u + 2) % 3];  // piece u - 1's
       float m = -CUDART_INF_F, l = 0.f;  // this group's last reference, its sum
       for (int i = PAIR ? 0 : (x0 + grp_w) & 1; i < len; i += PAIR ? 1 : 2) {
         const int x = x0 + i, k = count_of(x);
@@ -706,12 +713,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               float v[16];
               umma::ld16(s_col + e, v);
               if (p.use_softcap) {
+                float big = 0.f;  // NaN: not at all within the bound
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  float a, q;
-                  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(v[j] * cap_c));
-                  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + a));
-                  v[j] = fmaf(-cap_b, q, cap_a);
+                for (int j = 0; j < 16; ++j) big = (fabsf(v[j]) <= cap_lim) ? big : 1.f;
+                if (__any_sync(FULL, big != 0.f && real)) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    float a, q;
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(v[j] * cap_c));
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + a));
+                    v[j] = fmaf(-cap_b, q, cap_a);
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 16; j += 2) {
+                    const float2 a = make_float2(v[j], v[j + 1]), y = mul_f32x2(a, cap_y2), z = mul_f32x2(y, y);
+                    float2 t = make_float2(-1382.f / 155925.f, -1382.f / 155925.f);
+                    t = fma_f32x2(t, z, make_float2(62.f / 2835.f, 62.f / 2835.f));
+                    t = fma_f32x2(t, z, make_float2(-17.f / 315.f, -17.f / 315.f));
+                    t = fma_f32x2(t, z, make_float2(2.f / 15.f, 2.f / 15.f));
+                    t = fma_f32x2(t, z, make_float2(-1.f / 3.f, -1.f / 3.f));
+                    t = fma_f32x2(t, z, make_float2(1.f, 1.f));
+                    t = mul_f32x2(t, mul_f32x2(a, cap_s2));
+                    v[j] = t.x, v[j + 1] = t.y;
+                  }
                 }
               } else if (pre) {
 #pragma unroll
@@ -802,64 +827,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         } else if (!PAIR && lane == 0) {
           mbar_arrive(bar(sh.mready[quad][x & 1]));  // one arrival a tile, whoever reads
         }
-        if (masked) {
+        if (masked && (!PAIR || grp_w == 0)) {  // PAIR: V is mended once, and the first row tile's P V goes first
           ok = wait_use(sh.vfull[x % NV], x / NV);
           if (!ok) break;
           const uint32_t vst = v_s + (x % NV) * C::kKBytes;
           constexpr int CPR = C::kPanels * 8;  // 16-byte chunks of a row
-          constexpr int NT = PAIR ? 256 : 128;  // threads at it
-          const int me = PAIR ? tid : tid & 127;
-          auto chunk = [&](int idx) {  // of row idx / CPR; where a row's chunks are does not matter
-            const int e = idx / CPR, rem = idx % CPR;
-            return vst + (rem >> 3) * C::kKVPanelBytes + e * 128 + ((rem & 7) << 4);
-          };
-          // Rows of V that no row attends: zero (they were not loaded, or hold what stands behind the end).
-          auto clear = [&](int from, int to) {
-            for (int idx = from * CPR + me; idx < to * CPR; idx += NT)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(idx)), "r"(0u) : "memory");
-          };
-          clear(0, min(c.ulo - kt, TILE));
-          clear(max(L - kt, 0), TILE);
+          const int me = tid & 127;
+          // Rows of V that no row attends (they were not loaded, or hold what
+          // stands behind the end): zero.  Rows that some may attend and some
+          // not, the tree's and those at the windows' starts: see above.
+          uint64_t none = low_bits(min(max(c.ulo - kt, 0), TILE)) | ~low_bits(min(max(L - kt, 0), TILE));
           for (int e = 0; e < 4; ++e)
-            if ((skip >> e) & 1u) clear(16 * e, 16 * e + 16);
-          if (edge) {
-            // Rows that some may attend and some not: the tree's, those at the windows' starts.
-            const bool tree = kt + TILE > base, starts = kt < w_end;
-            const int slot = tree ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - kt0) / TILE;
-            const int end = (tree ? min(L - kt, TILE) : min(w_end - kt, TILE)) * CPR;
-            constexpr int U = 4;
+            if ((skip >> e) & 1u) none |= 0xffffull << (16 * e);
+          const bool tree = kt + TILE > base;
+          uint64_t some = tree ? ~low_bits(max(base - kt, 0)) : 0ull;
+          if (kt < w_end) some |= low_bits(min(w_end - kt, TILE));
+          some &= ~none;
+          const int slot = tree ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - kt0) / TILE;
+          constexpr int RPI = 128 / CPR;  // rows at a time
 #pragma unroll 1
-            for (int i0 = max(starts ? c.ulo - kt : base - kt, 0) * CPR + me; i0 < end; i0 += NT * U) {
-              uint32_t v[U][4], exps = 0;
+          for (int at = me / CPR; at < TILE; at += RPI) {
+            if (!(((none | some) >> at) & 1ull)) continue;
+            const uint32_t dst = vst + (me % CPR >> 3) * C::kKVPanelBytes + at * 128 + ((me & 7) << 4);
+            uint32_t v[4] = {0, 0, 0, 0};
+            bool change = (none >> at) & 1ull;
+            if (!change) {
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                           : "r"(dst));
 #pragma unroll
-              for (int e = 0; e < U; ++e) {
-                v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0;
-                if (i0 + NT * e < end)
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(v[e][0]), "=r"(v[e][1]), "=r"(v[e][2]), "=r"(v[e][3])
-                               : "r"(chunk(i0 + NT * e)));
+              for (int j = 0; j < 4; ++j) {  // exponent bits all set: not finite
+                if ((v[j] & 0x7f80u) == 0x7f80u) v[j] &= 0xffff0000u, change = true;
+                if ((v[j] & 0x7f800000u) == 0x7f800000u) v[j] &= 0xffffu, change = true;
               }
-#pragma unroll
-              for (int e = 0; e < U; ++e)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) exps = __vmaxu2(exps, v[e][j] & 0x7f807f80u);
-              // Exponent bits all set in some element: not finite.
-              if ((exps & 0xffffu) != 0x7f80u && (exps >> 16) != 0x7f80u) continue;
-              for (int e = 0; e < U; ++e) {
-                const int idx = i0 + NT * e, at = idx / CPR;
-                if (idx >= end || ((skip >> (at >> 4)) & 1u)) continue;
-                bool found = false;
-                for (int j = 0; j < 4; ++j) {
-                  if ((v[e][j] & 0x7f80u) == 0x7f80u) v[e][j] &= 0xffff0000u, found = true;
-                  if ((v[e][j] & 0x7f800000u) == 0x7f800000u) v[e][j] &= 0xffffu, found = true;
-                }
-                if (!found) continue;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(idx)), "r"(v[e][0]),
-                             "r"(v[e][1]), "r"(v[e][2]), "r"(v[e][3])
-                             : "memory");
-                atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << at);
-              }
+              if (change) atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << at);
             }
+            if (change)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                           "r"(v[3])
+                           : "memory");
           }
           fence_proxy_async_smem();  // visible to the tensor core's reads
         }
@@ -868,10 +874,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) mbar_arrive(bar(sh.pready[grp_w][k & 1]));
       }
       if (!ok || *abort_flag) break;
-
-      // The next piece, if it is known already: its masks come while this one's last P V runs.
-      taken = __all_sync(FULL, mbar_try_wait(bar(sh.pfull[(u + 1) % kTreePieces]), ((u + 1) / kTreePieces) & 1));
-      if (taken) take(u + 1);
+      // The piece after is in the ring by now, or comes without this warp's help.
+      ok = wait_use(sh.pfull[u % kTreePieces], u / kTreePieces);
+      if (!ok) break;
+      nxt = sh.pieces[u % kTreePieces];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
+      row_nxt = TreeRow{0, 0};
+      if (nxt.b >= 0) row_nxt = tree_row(p, TreeSeq{nxt.L, nxt.n, nxt.L - nxt.n}, nxt.b, node);
+      if (!work) {
+        if (nxt.b < 0) break;
+        continue;
+      }
 
       // ---- write the piece's rows -------------------------------------------------------
       const int last = x0 + len - 1, kl = count_of(last);
@@ -889,10 +903,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!PAIR && active) sh.l[grp_w][r] = l;
       // The next piece's marks, clear before any warp can be at that piece and
       // after every warp is past the piece that used them (three ago).
-      if (tid < 4) sh.bad[(u + 1) % 3][tid] = 0;
+      if (tid < 4) sh.bad[u % 3][tid] = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.epi));
-      ok = wait_use(sh.epi, u);
+      ok = wait_use(sh.epi, u - 1);
       if (!ok) break;
       if (!PAIR && active) l = sh.l[0][r] + sh.l[1][r];
       uint64_t marks = 0;
@@ -906,7 +920,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             ((int64_t)c.b * p.tree_len * p.hq + (int64_t)c.g * G + head) * D;
       if (active) {
         // Not PAIR: each group writes half of the columns.
-        constexpr int CH = PAIR ? D / 16 : D / 32, U = CH < 4 ? CH : 4;  // 16-column chunks, in flight
+        constexpr int CH = PAIR ? D / 16 : D / 32;  // 16-column chunks
         const int e0 = PAIR ? 0 : grp_w * CH;
         if (marks) {  // give back what was taken out of V, to the rows that attend it
 #pragma unroll 1
@@ -935,33 +949,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
 #pragma unroll 1
-        for (int e = e0; e < e0 + CH; e += U) {
-          uint32_t v[U][16];
-#pragma unroll
-          for (int z = 0; z < U; ++z) umma::ld16_nowait(o_col + (e + z) * 16, v[z]);
-          umma::wait_ld();
+        for (int e = e0; e < e0 + CH; ++e) {
+          float f[16];
+          umma::ld16(o_col + e * 16, f);
           if (!real) continue;
+          if (whole) {
+            uint32_t o[8];
 #pragma unroll
-          for (int z = 0; z < U; ++z) {
-            float f[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[z][j]);
-            if (whole) {
-              uint32_t o[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f[2 * j] * inv, f[2 * j + 1] * inv);
-              if (sectors) {
-                st_global_32(orow + (e + z) * 16, o);
-              } else {
-                reinterpret_cast<uint4*>(orow + (e + z) * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                reinterpret_cast<uint4*>(orow + (e + z) * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-              }
+            for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f[2 * j] * inv, f[2 * j + 1] * inv);
+            if (sectors) {
+              st_global_32(orow + e * 16, o);
             } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float4*>(po + (int64_t)((e + z) * 4 + j) * row_stride * 4) =
-                    make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+              reinterpret_cast<uint4*>(orow + e * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              reinterpret_cast<uint4*>(orow + e * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
             }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(po + (int64_t)(e * 4 + j) * row_stride * 4) =
+                  make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
           }
         }
         if (real && !whole && (PAIR || grp_w == 0))
@@ -970,6 +976,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       umma::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.ofree));
+      if (nxt.b < 0) break;
     }
     if (!ok) give_up();
   }
