@@ -400,15 +400,17 @@ pa_status_t pa_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   1 <= tree_len <= 64 (PA_ERR_UNSUPPORTED above).  bf16 runs on the tensor
  *   cores, fp32 on CUDA cores.
  *   workspace: for bf16, device memory of at least
- *   pa_decode_tree_workspace_size() bytes, 16-byte aligned, scratch within a
- *   call; it needs no zeroing.  The first 256 KiB (pa_decode_splitk's counter
- *   region) are left alone, so that a workspace may serve this call and
- *   pa_decode_splitk's family.  Calls that share a workspace must be ordered
- *   on one stream.  fp32: none (workspace may be NULL).
+ *   pa_decode_tree_workspace_size() bytes, 16-byte aligned, under
+ *   pa_decode_splitk's contract: its first PA_COUNTER_BYTES zero before its
+ *   first use, and left at zero by every call, so that one workspace serves
+ *   this call and pa_decode_splitk's family in any order; calls that share it
+ *   must be ordered on one stream; after PA_DEVERR_TIMEOUT zero it again.
+ *   fp32: none (workspace may be NULL).  Two launches for bf16, one for fp32.
  *   Passages: nano-vllm (ovshake) README, "Features" (speculative decoding)
  *   and the speculative-decoding command line (--num-speculative-tokens);
  *   attention over the cache as in "Key Concepts Explained: KV Cache".
  */
+#define PA_COUNTER_BYTES (2u * 131072u) /* 256 KiB, the workspaces' counter region */
 pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                            const int32_t* context_lens, const int32_t* tree_lens, const int64_t* tree_mask,
                            int64_t mask_stride, int32_t batch, int32_t tree_len, int32_t num_q_heads,

@@ -1,4 +1,5 @@
-"""ctypes binding of ``libpagedattn.so`` (include/pagedattn.h).
+"""Binding of ``libpagedattn.so`` (include/pagedattn.h): ctypes, and for the
+drafting step's calls, which run once a layer, a small native module.
 
 Argument marshalling only: shapes, raw device pointers and the current CUDA
 stream go to the C ABI; every step of the computation runs in the library's
@@ -43,7 +44,7 @@ def _load_library() -> ctypes.CDLL:
         try:
             path = _build.build()
         except Exception as e:  # noqa: BLE001
-            if not os.path.exists(path):
+            if not (os.path.exists(path) and os.path.exists(_build.NATIVE)):
                 raise ImportError(f"libpagedattn.so is missing and could not be built: {e}") from e
     lib = ctypes.CDLL(path)
     lib.pa_write_kv.argtypes = [_c_vp, _c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
@@ -366,54 +367,20 @@ def prefill(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torc
     return out
 
 
-def _same(what: str, dtype: torch.dtype, device: torch.device, *tensors: Optional[torch.Tensor]) -> None:
-    """Every tensor given has this type and lies on this CUDA device."""
-    for t in tensors:
-        if t is not None and (t.dtype != dtype or t.device != device):
-            raise ValueError(f"{what}: expected {dtype} on {device}, got {t.dtype} on {t.device}")
-    if device.type != "cuda":
-        raise ValueError(f"{what}: tensors must be on a CUDA device")
+_native_module = None
 
 
-def _rows(t: torch.Tensor, heads: int, d: int) -> int:
-    """Elements between the token rows of a ``[N, heads, d]`` tensor whose rows are contiguous."""
-    if t.shape[1:] != (heads, d) or t.dim() != 3:
-        raise ValueError(f"expected [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    row, head, one = t.stride()
-    if one != 1 or (head != d and heads > 1):
-        raise ValueError("a token's heads must be contiguous")
-    return row if t.shape[0] > 1 else heads * d
+def _native():
+    """The module that looks at the tensors of the per-step calls and makes them
+    (csrc/native_binding.cpp), opened with the library on first use."""
+    global _native_module
+    if _native_module is None:
+        _lib()
+        from . import _native as module
 
-
-def _launch(device: torch.device, what: str, fn, args, stream) -> None:
-    """Call ``fn`` with ``device`` current, on ``stream`` (None: the device's current stream)."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
-    if st != PA_OK:
-        raise PagedAttnError(st, what)
-
-
-def _rope_inputs(what, q, k, positions, inv_freq, q_weight, k_weight, rotary_dim):
-    """Checked shapes: (tokens, q heads, kv heads, head_dim, rotary_dim)."""
-    n, hq, d = q.shape
-    hkv = k.shape[1]
-    if k.shape[0] != n:
-        raise ValueError(f"{what}: q has {n} tokens, k {k.shape[0]}")
-    _same(what, q.dtype, q.device, k)
-    _same(what, torch.float32, q.device, inv_freq, q_weight, k_weight)
-    _same(what, torch.int32, q.device, positions)
-    rd = 2 * inv_freq.numel() if inv_freq is not None else 0
-    if rotary_dim is not None and rotary_dim != rd:
-        raise ValueError(f"{what}: inv_freq has {rd // 2} frequencies, rotary_dim / 2 are needed")
-    if rd and (positions is None or positions.numel() != n):
-        raise ValueError(f"{what}: one position per token is needed")
-    for w in (q_weight, k_weight):
-        if w is not None and w.numel() != d:
-            raise ValueError(f"{what}: a norm weight has head_dim elements")
-    return n, hq, hkv, d, rd
+        module.set_error_class(PagedAttnError)
+        _native_module = module
+    return _native_module
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor],
@@ -426,19 +393,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     a fused projection).  ``positions``: int32 ``[N]``; ``inv_freq``: fp32
     ``[rotary_dim / 2]`` (None: norm only); weights: fp32 ``[D]``.  ``q_out`` may
     be ``q`` and ``k_out`` ``k``.  Returns ``(q_out, k_out)``."""
-    n, hq, hkv, d, rd = _rope_inputs("qk_norm_rope", q, k, positions, inv_freq, q_weight, k_weight, rotary_dim)
-    if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty((n, hkv, d), dtype=q.dtype, device=q.device)
-    _same("qk_norm_rope", q.dtype, q.device, q_out, k_out)
-    if q_out.shape[0] != n or k_out.shape[0] != n:
-        raise ValueError("qk_norm_rope: outputs have the inputs' shapes")
-    _launch(q.device, "pa_qk_norm_rope", _lib().pa_qk_norm_rope,
-            (q.data_ptr(), _rows(q, hq, d), k.data_ptr(), _rows(k, hkv, d), _ptr(q_weight), _ptr(k_weight), eps,
-             _ptr(inv_freq), rd, 1 if interleaved else 0, _ptr(positions), n, hq, hkv, d, q_out.data_ptr(),
-             _rows(q_out, hq, d), k_out.data_ptr(), _rows(k_out, hkv, d), _dtype_code(q)), stream)
-    return q_out, k_out
+    return (_native_module or _native()).qk_norm_rope(q, k, positions, inv_freq, rotary_dim, q_weight, k_weight, eps,
+                                                      interleaved, q_out, k_out, stream)
 
 
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
@@ -450,24 +406,8 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Op
     values ``v`` ``[N, Hkv, D]`` go to the caches at ``slot_mapping`` (int64;
     negative: a padding token, nothing of which is written), the rotated queries
     to ``q_out`` ``[N, Hq, D]`` (contiguous; may be ``q``).  Returns ``q_out``."""
-    n, hq, hkv, d, rd = _rope_inputs("rope_append", q, k, positions, inv_freq, q_weight, k_weight, rotary_dim)
-    nb, hkv_c, bs, d_c = k_cache.shape
-    if (hkv_c, d_c) != (hkv, d) or v_cache.shape != k_cache.shape or v.shape != k.shape:
-        raise ValueError("rope_append: k, v and the caches must agree in kv heads and head_dim")
-    if slot_mapping.numel() != n:
-        raise ValueError("rope_append: one slot per token is needed")
-    if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("rope_append: q_out has q's shape")
-    _same("rope_append", q.dtype, q.device, v, k_cache, v_cache, q_out)
-    _same("rope_append", torch.int64, q.device, slot_mapping)
-    _launch(q.device, "pa_rope_append", _lib().pa_rope_append,
-            (q.data_ptr(), _rows(q, hq, d), k.data_ptr(), _rows(k, hkv, d), v.data_ptr(), _rows(v, hkv, d),
-             _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), rd, 1 if interleaved else 0, _ptr(positions),
-             _ptr(slot_mapping), n, hq, hkv, d, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), nb, bs, _dtype_code(q)),
-            stream)
-    return q_out
+    return (_native_module or _native()).rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache,
+                                                     rotary_dim, q_weight, k_weight, eps, interleaved, q_out, stream)
 
 
 def decode_tree_workspace_size(batch: int, tree_len: int, num_q_heads: int, head_dim: int, max_context_len: int,
@@ -487,41 +427,12 @@ def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     drafts; bit i of node j's word says that j attends node i (its ancestors and
     itself).  ``tree_lens`` (int32 ``[B]``): nodes of each sequence's tree, when
     they have fewer than T (the rows of the others are zero).  The workspace
-    needs no zeroing; it is allocated with torch if not given.
+    must be zero-filled before its first use, as ``decode_splitk``'s; it is
+    allocated with torch, its counter region zeroed, if not given.
     """
-    B, T, hq, d = q.shape
-    nb, hkv, bs, d_c = k_cache.shape
-    if d_c != d or v_cache.shape != k_cache.shape:
-        raise ValueError("decode_tree: q and the caches must agree in head_dim")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
-        raise ValueError("decode_tree: one table row and one length per sequence are needed")
-    if tree_mask.shape == (B, T):
-        mask_stride = T
-    elif tree_mask.shape == (T,):
-        mask_stride = 0
-    else:
-        raise ValueError(f"decode_tree: tree_mask is [batch, nodes] or [nodes], got {tuple(tree_mask.shape)}")
-    if tree_lens is not None and tree_lens.numel() != B:
-        raise ValueError("decode_tree: one tree length per sequence is needed")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif out.shape != q.shape:
-        raise ValueError("decode_tree: out has q's shape")
-    device = q.device
-    _same("decode_tree", q.dtype, device, k_cache, v_cache, out)
-    _same("decode_tree", torch.int32, device, block_tables, context_lens, tree_lens)
-    _same("decode_tree", torch.int64, device, tree_mask)
-    if workspace is None:
-        need = _lib().pa_decode_tree_workspace_size(B, T, hq, d, max_context_len, hkv) if q.dtype == torch.bfloat16 else 0
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError("decode_tree: the workspace is on another device")
-    _launch(device, "pa_decode_tree", _lib().pa_decode_tree,
-            (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(tree_lens),
-             _ptr(tree_mask), mask_stride, B, T, hq, hkv, d, bs, block_tables.shape[1], nb, scale, softcap, window,
-             _ptr(out), _dtype_code(q), max_context_len, _ptr(workspace),
-             workspace.numel() * workspace.element_size()), stream)
-    return out
+    return (_native_module or _native()).decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, scale,
+                                                     softcap, window, max_context_len, tree_lens, out, workspace,
+                                                     stream)
 
 
 def commit_tree(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -537,27 +448,8 @@ def commit_tree(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     ``tree_lens``: nodes of the trees, as in ``decode_tree``.  Returns the new
     context lengths (``new_lens``, int32 ``[B]``; not ``context_lens`` itself).
     """
-    if k_cache.dim() not in (4, 5) or v_cache.shape != k_cache.shape:
-        raise ValueError("commit_tree: caches are [blocks, kv heads, block_size, head_dim], or have layers before that")
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    nb, hkv, bs, d = k_cache.shape[-4:]
-    B = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or accepted.dim() != 2 or accepted.shape[0] != B:
-        raise ValueError("commit_tree: one table row and one path per sequence are needed")
-    if accept_lens.numel() != B or (tree_lens is not None and tree_lens.numel() != B):
-        raise ValueError("commit_tree: one length per sequence is needed")
-    device = k_cache.device
-    if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=device)
-    elif new_lens.numel() != B:
-        raise ValueError("commit_tree: one new length per sequence is needed")
-    _same("commit_tree", k_cache.dtype, device, v_cache)
-    _same("commit_tree", torch.int32, device, block_tables, context_lens, tree_lens, accepted, accept_lens, new_lens)
-    _launch(device, "pa_commit_tree", _lib().pa_commit_tree,
-            (_ptr(k_cache), _ptr(v_cache), layers, _ptr(block_tables), _ptr(context_lens), _ptr(tree_lens), tree_len,
-             _ptr(accepted), accepted.shape[1], _ptr(accept_lens), B, hkv, d, bs, block_tables.shape[1], nb,
-             _ptr(new_lens), _dtype_code(k_cache)), stream)
-    return new_lens
+    return (_native_module or _native()).commit_tree(k_cache, v_cache, block_tables, context_lens, accepted,
+                                                     accept_lens, tree_len, tree_lens, new_lens, stream)
 
 
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor, stream=None) -> None:

@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,9 @@ MAIN = os.path.join(CSRC, "pagedattn.cu")
 # the drafting step's operators and theirs, and the host block manager.
 UNITS = [MAIN, os.path.join(CSRC, "tree_ops.cu"), os.path.join(CSRC, "block_manager.cpp")]
 OBJ_DIR = os.path.join(PKG, "_build")
+# The Python entry of the per-step calls (host code, linked to torch and to LIB).
+NATIVE_SRC = os.path.join(CSRC, "native_binding.cpp")
+NATIVE = os.path.join(PKG, "_native" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 NVCC_FLAGS = [
     "-gencode",
@@ -46,9 +50,9 @@ def sources() -> list:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(NATIVE)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
@@ -81,18 +85,54 @@ def _compile(unit: str, force: bool, verbose: bool, extra_flags) -> str:
     return obj
 
 
+def _torch_flags() -> tuple:
+    """Include paths and link flags of the installed torch."""
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [sysconfig.get_paths()["include"], "/usr/local/cuda/include", *cpp_extension.include_paths()]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
+    return ([abi, *[x for d in inc for x in ("-isystem", d)]],
+            ["-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+
+
+def _compile_native(force: bool, verbose: bool) -> str:
+    obj = _object(NATIVE_SRC)
+    if not force and _fresh(obj):
+        return obj
+    tmp = f"{obj}.tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *_torch_flags()[0], "-MMD", "-MF", tmp + ".d", "-MT", "object", "-c",
+           "-o", tmp, NATIVE_SRC]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp + ".d", obj + ".d")
+    os.replace(tmp, obj)
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
-    with ThreadPoolExecutor(len(UNITS)) as pool:
+    with ThreadPoolExecutor(len(UNITS) + 1) as pool:
+        native = pool.submit(_compile_native, force, verbose)
         objs = list(pool.map(lambda u: _compile(u, force, verbose, extra_flags), UNITS))
+        native = native.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, native, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           *_torch_flags()[1]]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, NATIVE)
     return LIB
 
 

@@ -14,6 +14,8 @@
 
 namespace {
 
+static_assert(PA_COUNTER_BYTES == pa::kCounterBytes, "the header's size of the counter region");
+
 using pa::NormRopeParams;
 using pa::TreeParams;
 

@@ -118,8 +118,6 @@ def test_binding_refuses_mismatched_tensors():
         a.update(bad)
         with pytest.raises(ValueError):
             pa.rope_append(q, k, a["v"], pos, a["slots"], inv, a["kc"], a["kc"].clone())
-    with pytest.raises(ValueError):
-        bnd._rows(torch.zeros(4, 64, 8).transpose(1, 2), 8, 64)
     qt, bt, cl = torch.zeros(3, 5, 8, 64, dtype=bf), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
     mask = torch.zeros(3, 5, dtype=torch.int64)
     for bad in (dict(mask=mask[:2]), dict(mask=mask.int()), dict(bt=bt[:2]), dict(cl=cl.long()),

@@ -237,7 +237,7 @@ def test_a_chain_is_the_causal_multi_query_call(heads, nodes):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_where_the_blocks_lie_does_not_matter(dtype):
-    """The same bits for another placement, for a repeated call and whatever the workspace holds."""
+    """The same bits for another placement, for a repeated call and whatever the workspace holds behind its counters."""
     c = _case([100, 333, 64, 17], 10, (32, 8, 128), dtype, seed=15)
     out = _run(c)
     nb = c["k_cache"].shape[0]
@@ -252,8 +252,10 @@ def test_where_the_blocks_lie_does_not_matter(dtype):
     assert torch.equal(bits(_run(moved)), bits(out))
     need = pa.decode_tree_workspace_size(4, 10, 32, 128, 333, 8)
     ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
+    ws[:256 * 1024] = 0
     for _ in range(3):
         assert torch.equal(bits(_run(c, workspace=ws)), bits(out))
+    assert torch.count_nonzero(ws[:256 * 1024]).item() == 0
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -324,7 +326,7 @@ def test_strided_pool_offsets_past_32_bits():
 def test_other_stream_and_captured_graph(dtype):
     c = _case([100, 333, 64, 17], 10, (32, 8, 128), dtype, seed=23, fill=0.5)
     want = _run(c)
-    ws = torch.empty(max(16, pa.decode_tree_workspace_size(4, 10, 32, 128, 333, 8)), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(max(16, pa.decode_tree_workspace_size(4, 10, 32, 128, 333, 8)), dtype=torch.uint8, device="cuda")
     out = torch.zeros_like(want)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
