@@ -15,15 +15,17 @@
 // 131072.)
 //
 // The work is one read and one write of every row, so DRAM bounds it, and for
-// a decode step's few tokens the launch.  A head's row is held by D / 8
-// neighbouring lanes, 8 elements each (16-byte accesses for bf16): the norm's
-// sum is a shuffle over those lanes, and the half-split pair's other element
-// comes by a shuffle from the lane that holds it, so that every lane reads and
-// writes only its own 8 elements (which makes in-place calls safe).  A CTA
-// takes one token: its rotary / 2 angles are computed once, by as many
-// threads, into shared memory, and each lane keeps the eight it needs in
-// registers over all of its rows, since a lane sits at the same place of each.
-// Few tokens: the rows of a token are split over several CTAs.
+// a decode step's few tokens the launch.  A warp takes one token, or a part of
+// its rows where there are few tokens, on its own: no barrier joins warps, and
+// each has several rows in flight ahead of the one it works on.  A head's row is
+// held by D / 8 neighbouring lanes, each with four pairs: two chunks of four
+// elements (8-byte accesses for bf16), so that nothing but the norm's sum
+// passes between lanes, and a lane reads and writes only its own elements
+// (which makes in-place calls safe).  (With eight neighbouring elements a lane and
+// the pairs' other halves by shuffles, 16384 tokens of 48 rows of 128 took 83 us
+// instead of 74, 0.83 of the copy rate; with 4 or 10 CTAs an SM 83 and 104.)  The token's rotary / 2 angles are computed once, two or so a
+// lane, and pass through shared memory; a lane sits at the same place of each
+// of its rows and keeps the four it needs in registers.
 #pragma once
 
 #include "decode_common.cuh"
@@ -46,171 +48,166 @@ struct NormRopeParams {
   void *k_cache, *v_cache;                // APPEND: [blocks][hkv][block_size][D]
   int64_t num_slots;
   int block_size;
-  int rows_per_cta;
+  int tokens;
+  int parts, part_rows;                   // warps per token, rows of each (a multiple of the rows a warp holds)
 };
 
-constexpr int kNormRopeThreads = 256;
+constexpr int kNormRopeWarps = 4;
 
-// Eight consecutive elements of a row, as loaded (one 16-byte word for bf16, two for fp32).
+// Four consecutive elements, as they lie in memory.
 template <typename T>
-struct Raw8;
+struct Raw4;
 template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const void* src) { a = *static_cast<const uint4*>(src); }
-  __device__ __forceinline__ void store(void* dst) const { *static_cast<uint4*>(dst) = a; }
-  __device__ __forceinline__ void widen(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(w[i]);
-      x[2 * i + 1] = bf16_hi(w[i]);
-    }
-  }
-  __device__ __forceinline__ void round(const float (&x)[8]) {  // to nearest even
-    a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+struct Raw4<__nv_bfloat16> {
+  uint2 a;
+  __device__ __forceinline__ void load(const void* src) { a = *static_cast<const uint2*>(src); }
+  __device__ __forceinline__ void store(void* dst) const { *static_cast<uint2*>(dst) = a; }
+  __device__ __forceinline__ float4 wide() const { return make_float4(bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y)); }
+  __device__ __forceinline__ void round(float4 x) {  // to nearest even
+    a = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   }
 };
 template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* src) {
-    a = static_cast<const float4*>(src)[0];
-    b = static_cast<const float4*>(src)[1];
-  }
-  __device__ __forceinline__ void store(void* dst) const {
-    static_cast<float4*>(dst)[0] = a;
-    static_cast<float4*>(dst)[1] = b;
-  }
-  __device__ __forceinline__ void widen(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  __device__ __forceinline__ void round(const float (&x)[8]) {
-    a = make_float4(x[0], x[1], x[2], x[3]);
-    b = make_float4(x[4], x[5], x[6], x[7]);
-  }
+struct Raw4<float> {
+  float4 a;
+  __device__ __forceinline__ void load(const void* src) { a = *static_cast<const float4*>(src); }
+  __device__ __forceinline__ void store(void* dst) const { *static_cast<float4*>(dst) = a; }
+  __device__ __forceinline__ float4 wide() const { return a; }
+  __device__ __forceinline__ void round(float4 x) { a = x; }
 };
+
+__device__ __forceinline__ float4 scale4(float4 x, float s, float4 w) {
+  return make_float4(x.x * s * w.x, x.y * s * w.y, x.z * s * w.z, x.w * s * w.w);
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+}
+// a cos - b sin, b cos + a sin.
+__device__ __forceinline__ float4 turn4(float4 a, float4 b, float4 c, float4 s) {
+  return make_float4(fmaf(-b.x, s.x, a.x * c.x), fmaf(-b.y, s.y, a.y * c.y), fmaf(-b.z, s.z, a.z * c.z),
+                     fmaf(-b.w, s.w, a.w * c.w));
+}
+__device__ __forceinline__ float4 back4(float4 a, float4 b, float4 c, float4 s) {
+  return make_float4(fmaf(a.x, s.x, b.x * c.x), fmaf(a.y, s.y, b.y * c.y), fmaf(a.z, s.z, b.z * c.z),
+                     fmaf(a.w, s.w, b.w * c.w));
+}
 
 template <typename T, int D, bool APPEND>
-__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const NormRopeParams p) {
   constexpr uint32_t FULL = 0xffffffffu;
-  constexpr int LPR = D / 8;                        // lanes per row
-  constexpr int RPI = kNormRopeThreads / LPR;       // rows per iteration of the CTA
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;         // rows a lane loads before it works on the first
-  __shared__ float2 turn[D / 2];                    // (cos, sin) of the token's angles
+  constexpr int LPR = D / 8;                 // lanes per row
+  constexpr int RPW = 32 / LPR;              // rows a warp holds at a time
+  constexpr int U = sizeof(T) == 2 ? 4 : 3;  // of those, in flight
+  __shared__ __align__(16) float cosines[kNormRopeWarps][D / 2], sines[kNormRopeWarps][D / 2];  // of a warp's token
 
   pdl_launch_dependents();
-  pdl_wait();  // a programmatic dependent: nothing of global memory is touched before
-  const int64_t token = blockIdx.x;
-  const int tid = threadIdx.x, ch = tid % LPR;
+  const int lane = threadIdx.x & 31, ch = lane % LPR, warp = threadIdx.x >> 5;
+  const int64_t task = (int64_t)blockIdx.x * kNormRopeWarps + warp;
+  const int64_t token = task / p.parts;
+  if (token >= p.tokens) return;
   const int half = p.rotary >> 1;
+  pdl_wait();  // a programmatic dependent: nothing of global memory is touched before
 
-  int64_t slot = 0;
-  if (APPEND) {
-    slot = p.slots[token];
-    if (slot < 0) return;  // a padding token: none of its rows is written
-  }
-  const bool in_pool = !APPEND || slot < p.num_slots;
-  if (APPEND && !in_pool && tid == 0 && blockIdx.y == 0) raise_error(PA_DEVERR_SLOT);
+  // This lane's two chunks: the first and second elements of the pairs 4 ch .. 4 ch + 3
+  // (half-split; behind `rotary` the halves of what is left), or eight neighbours
+  // (interleaved: two pairs in each).
+  const bool rotated = p.interleaved ? ch * 8 < p.rotary : ch * 4 < half;
+  const int rest = ch * 4 - half;
+  const int lo = p.interleaved ? ch * 8 : rotated ? ch * 4 : p.rotary + rest;
+  const int hi = p.interleaved ? lo + 4 : rotated ? lo + half : lo + ((D - p.rotary) >> 1);
 
-  // ---- this CTA's rows: q heads, then k heads, then (APPEND) v heads -----------------------
+  // ---- this warp's rows: q heads, then k heads, then (APPEND) v heads -----------------------
+  const int64_t slot = APPEND ? p.slots[token] : 0;
+  const double position = p.rotary > 0 ? (double)p.positions[token] : 0.0;
   const int rows = p.hq + (APPEND ? 2 : 1) * p.hkv;
-  const int r_begin = blockIdx.y * p.rows_per_cta + tid / LPR;
-  const int r_end = min(rows, ((int)blockIdx.y + 1) * p.rows_per_cta);
-  const T* q = static_cast<const T*>(p.q) + token * p.q_stride + ch * 8;
-  const T* k = static_cast<const T*>(p.k) + token * p.k_stride + ch * 8;
-  const T* v = APPEND ? static_cast<const T*>(p.v) + token * p.v_stride + ch * 8 : nullptr;
+  const int begin = (int)(task - token * p.parts) * p.part_rows;  // the same in all lanes
+  const int end = min(rows, begin + p.part_rows);
+  const T* q = static_cast<const T*>(p.q) + token * p.q_stride;
+  const T* k = static_cast<const T*>(p.k) + token * p.k_stride;
+  const T* v = APPEND ? static_cast<const T*>(p.v) + token * p.v_stride : nullptr;
   auto source = [&](int r) -> const T* {
     if (r < p.hq) return q + (int64_t)r * D;
     if (!APPEND || r < p.hq + p.hkv) return k + (int64_t)(r - p.hq) * D;
     return v + (int64_t)(r - p.hq - p.hkv) * D;
   };
+  Raw4<T> a[U], b[U];
+  const int mine = lane / LPR;  // which of the warp's rows
+  auto load = [&](int u, int r) {
+    const T* x = source(r);
+    a[u].load(x + lo);
+    b[u].load(x + hi);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)  // in flight while the angles are computed
+    if (begin + u * RPW + mine < end) load(u, begin + u * RPW + mine);
+
+  for (int i = lane; i < half; i += 32) {
+    const double t = position * ((double)p.inv_freq[i] * 0.15915494309189535);  // turns: 1 / (2 pi)
+    sincospif(2.f * (float)(t - rint(t)), &sines[warp][i], &cosines[warp][i]);
+  }
+  __syncwarp();
+  if (APPEND && slot < 0) return;  // a padding token: none of its rows is written
+  const bool in_pool = !APPEND || slot < p.num_slots;
+  if (APPEND && !in_pool && lane == 0 && begin == 0) raise_error(PA_DEVERR_SLOT);
   const int64_t blk = APPEND ? slot / p.block_size : 0;
   const int64_t off = APPEND ? slot - blk * p.block_size : 0;
   auto target = [&](int r) -> T* {
-    if (r < p.hq) return static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)r * D + ch * 8;
-    if (!APPEND) return static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)(r - p.hq) * D + ch * 8;
+    if (r < p.hq) return static_cast<T*>(p.q_out) + token * p.q_out_stride + (int64_t)r * D;
+    if (!APPEND) return static_cast<T*>(p.k_out) + token * p.k_out_stride + (int64_t)(r - p.hq) * D;
     const bool is_k = r < p.hq + p.hkv;
     const int64_t h = r - p.hq - (is_k ? 0 : p.hkv);
-    return static_cast<T*>(is_k ? p.k_cache : p.v_cache) + ((blk * p.hkv + h) * p.block_size + off) * D + ch * 8;
+    return static_cast<T*>(is_k ? p.k_cache : p.v_cache) + ((blk * p.hkv + h) * p.block_size + off) * D;
   };
 
-  Raw8<T> raw[U];
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u * RPI < r_end) raw[u].load(source(r0 + u * RPI));
-  };
-  load(r_begin);  // in flight while the angles are computed
-
-  if (tid < half) {
-    const double turns = (double)p.positions[token] * ((double)p.inv_freq[tid] * 0.15915494309189535);  // 1 / (2 pi)
-    float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    turn[tid] = make_float2(c, s);
-  }
-  __syncthreads();
-
-  // This lane's eight elements: their angles, and the lane that holds their pairs.
-  const bool rotated = ch * 8 < p.rotary;
-  const bool second = !p.interleaved && ch * 8 >= half;  // second elements of half-split pairs
-  int mate = tid & 31;
-  float c8[8], s8[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) c8[e] = 1.f, s8[e] = 0.f;
-  if (rotated) {
-    if (!p.interleaved) mate += second ? -(half >> 3) : (half >> 3);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 t = turn[p.interleaved ? ch * 4 + e / 2 : ch * 8 + e - (second ? half : 0)];
-      c8[e] = t.x;
-      s8[e] = (p.interleaved ? (e & 1) != 0 : second) ? t.y : -t.y;
-    }
+  // This lane's angles: four pairs, or (interleaved) two pairs' in each chunk, both elements' the same.
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (rotated) {  // half-split: pair 4 ch + e; interleaved: chunk elements (2 e, 2 e + 1) are pair 4 ch + e
+    c = *reinterpret_cast<const float4*>(&cosines[warp][ch * 4]);
+    sn = *reinterpret_cast<const float4*>(&sines[warp][ch * 4]);
   }
 
-  // Every lane of a warp makes the same number of iterations (the shuffles are warp-wide).
-  for (int r0 = r_begin; __any_sync(FULL, r0 < r_end); r0 += U * RPI) {
-    if (r0 != r_begin) load(r0);
+  for (int r0 = begin; r0 < end; r0 += U * RPW) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * RPI;
-      const bool real = r < r_end;
-      const bool turned = r < p.hq + p.hkv;  // v rows are copied as they are
-      if (!__any_sync(FULL, real)) break;
-      if (__any_sync(FULL, real && turned)) {
-        float x[8], y[8];
-        if (real) {
-          raw[u].widen(x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        }
-        const float* w = r < p.hq ? p.q_weight : p.k_weight;
-        const bool norm = turned && w;
-        if (__any_sync(FULL, norm)) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      const int first = r0 + u * RPW, r = first + mine;  // `first`: the same in all lanes
+      if (first >= end) break;
+      const bool real = r < end;
+      if (first < p.hq + p.hkv) {  // some row is of q or k; v rows are copied as they are
+        const bool turned = r < p.hq + p.hkv;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (real) x = a[u].wide(), y = b[u].wide();
+        if (p.q_weight || p.k_weight) {
+          float ss = dot4(x, x) + dot4(y, y);
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-          if (norm) {
+          const float* w = r < p.hq ? p.q_weight : p.k_weight;
+          if (turned && w) {
             const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-            const float4 wa = *reinterpret_cast<const float4*>(w + ch * 8);
-            const float4 wb = *reinterpret_cast<const float4*>(w + ch * 8 + 4);
-            const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wv[e];
+            x = scale4(x, inv, *reinterpret_cast<const float4*>(w + lo));
+            y = scale4(y, inv, *reinterpret_cast<const float4*>(w + hi));
           }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = p.interleaved ? x[e ^ 1] : __shfl_sync(FULL, x[e], mate);
-          y[e] = rotated ? fmaf(other, s8[e], x[e] * c8[e]) : x[e];
+        float4 xr, yr;
+        if (p.interleaved) {
+          xr = make_float4(fmaf(-x.y, sn.x, x.x * c.x), fmaf(x.x, sn.x, x.y * c.x), fmaf(-x.w, sn.y, x.z * c.y),
+                           fmaf(x.z, sn.y, x.w * c.y));
+          yr = make_float4(fmaf(-y.y, sn.z, y.x * c.z), fmaf(y.x, sn.z, y.y * c.z), fmaf(-y.w, sn.w, y.z * c.w),
+                           fmaf(y.z, sn.w, y.w * c.w));
+        } else {
+          xr = turn4(x, y, c, sn);
+          yr = back4(x, y, c, sn);
         }
-        if (turned) raw[u].round(y);
+        if (turned) {  // (not rotated: as it is, since 0 times an infinity is not nothing)
+          a[u].round(rotated ? xr : x);
+          b[u].round(rotated ? yr : y);
+        }
       }
-      if (real && (in_pool || r < p.hq)) raw[u].store(target(r));
+      if (real && (in_pool || r < p.hq)) {
+        T* out = target(r);
+        a[u].store(out + lo);
+        b[u].store(out + hi);
+      }
+      if (r + U * RPW < end) load(u, r + U * RPW);
     }
   }
 }

@@ -23,16 +23,19 @@ using pa::TreeParams;
 
 template <typename T, int D, bool APPEND>
 cudaError_t launch_norm_rope_t(NormRopeParams& p, int32_t tokens, cudaStream_t st) {
-  constexpr int kRowsPerIter = pa::kNormRopeThreads / (D / 8);
+  constexpr int kRows = 32 / (D / 8);  // that a warp holds at a time
   const int rows = p.hq + (APPEND ? 2 : 1) * p.hkv;
-  const int iters = (rows + kRowsPerIter - 1) / kRowsPerIter;
-  // One CTA per token; the rows of a token over several CTAs while there are
-  // fewer than two CTAs per SM.
-  const int split = (int)std::min<long long>(iters, (2LL * sm_count() + tokens - 1) / tokens);
+  const int iters = (rows + kRows - 1) / kRows;
+  // A warp per token; a token's rows over several warps while there are fewer
+  // than 64 per SM, two for each place (a few tokens: a warp for each 32 lanes' rows).
+  const int split = (int)std::min<long long>(iters, (64LL * sm_count() + tokens - 1) / tokens);
   const int per = (iters + split - 1) / split;
-  p.rows_per_cta = per * kRowsPerIter;
-  const dim3 grid((unsigned)tokens, (unsigned)((iters + per - 1) / per));
-  return launch_ex(pa::norm_rope_kernel<T, D, APPEND>, grid, dim3(pa::kNormRopeThreads), 0, st, true, p);
+  p.tokens = tokens;
+  p.part_rows = per * kRows;
+  p.parts = (iters + per - 1) / per;
+  const long long tasks = (long long)tokens * p.parts;
+  const dim3 grid((unsigned)((tasks + pa::kNormRopeWarps - 1) / pa::kNormRopeWarps));
+  return launch_ex(pa::norm_rope_kernel<T, D, APPEND>, grid, dim3(pa::kNormRopeWarps * 32), 0, st, true, p);
 }
 
 template <bool APPEND>
@@ -84,21 +87,21 @@ pa_status_t check_norm_rope(const NormRopeParams& p, int32_t num_tokens, int32_t
 
 // ---- tree attention -------------------------------------------------------------------
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_tree_simt_t(const TreeParams& p, cudaStream_t st) {
-  constexpr int RT = pa::kTreeSimtRows, NW = pa::kTreeSimtWarps;
+  constexpr int RT = pa::kTreeSimtRows;
   const dim3 grid((unsigned)((p.tree_len * p.group + RT - 1) / RT), p.hkv, p.batch);
-  return launch_ex(pa::decode_tree_simt_kernel<T, D>, grid, dim3(NW * 32), NW * RT * D * 4, st, true, p);
+  return launch_ex(pa::decode_tree_simt_kernel<D>, grid, dim3(pa::kTreeSimtWarps * 32), 0, st, true, p);
 }
 
 cudaError_t launch_tree_simt(const TreeParams& p, int head_dim, cudaStream_t st) {
   switch (head_dim) {
     case 64:
-      return launch_tree_simt_t<float, 64>(p, st);
+      return launch_tree_simt_t<64>(p, st);
     case 128:
-      return launch_tree_simt_t<float, 128>(p, st);
+      return launch_tree_simt_t<128>(p, st);
     default:
-      return launch_tree_simt_t<float, 256>(p, st);
+      return launch_tree_simt_t<256>(p, st);
   }
 }
 
