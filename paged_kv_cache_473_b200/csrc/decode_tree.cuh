@@ -668,17 +668,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     bool ok = true;
     int x0 = 0;  // the CTA's tiles before this piece
     TreePiece c, nxt;
-    TreeRow row, row_nxt;
+    uint64_t word = 0;  // this row's mask word in the next piece
     nxt.b = -1;
-    // Turn u: the tiles of piece u - 1, the next piece's masks (they come while the
-    // last P V runs), then the rows of piece u - 1.
+    // Turn u: the tiles of piece u - 1, the next piece's mask words (they come while
+    // the last P V runs), then the rows of piece u - 1.
     for (int u = 0; ok; ++u) {
       c = nxt;
-      row = row_nxt;
       const bool work = u > 0;
       const int rows = max(0, min(p.q_nodes, c.n - mt * p.q_nodes)) * G;
       const bool real = r < rows, active = 32 * quad < rows;
       const int L = c.L, base = L - c.n, kt0 = c.ulo & ~(TILE - 1), len = work ? c.t1 - c.t0 : 0;
+      const TreeRow row = work ? tree_row(p, TreeSeq{L, c.n, base}, c.b, node, word) : TreeRow{0, 0};
       // Rows' windows start in [ulo, ulo + 63] (a depth is at most 63) and at most at base.
       const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;
       uint64_t* bad = sh.bad[(u + 2) % 3];  // piece u - 1's
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int i = PAIR ? 0 : (x0 + grp_w) & 1; i < len; i += PAIR ? 1 : 2) {
         const int x = x0 + i, k = count_of(x);
         ok = wait_use(sh.sfull[grp_w][k & 1], k >> 1);
-        if (!ok || *abort_flag) break;
+        if (!ok) break;
         umma::fence_after();
         const int kt = kt0 + (c.t0 + i) * TILE;
         const uint32_t skip = *const_cast<volatile uint8_t*>(&sh.skip[x % C::kRing]);
@@ -750,12 +750,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           float y[TILE];
           {
-            uint32_t v[TILE / 16][16];
+            uint32_t v[TILE / 32][32];
 #pragma unroll
-            for (int e = 0; e < TILE / 16; ++e) umma::ld16_nowait(s_col + e * 16, v[e]);
+            for (int e = 0; e < TILE / 32; ++e) umma::ld32_nowait(s_col + e * 32, v[e]);
             umma::wait_ld();
 #pragma unroll
-            for (int e = 0; e < TILE; ++e) y[e] = __uint_as_float(v[e / 16][e % 16]);
+            for (int e = 0; e < TILE; ++e) y[e] = __uint_as_float(v[e / 32][e % 32]);
           }
           float mx[8];
 #pragma unroll
@@ -787,8 +787,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (lane == 0) mbar_arrive(bar(sh.mready[quad][x & 1]));
           }
           const float ref = now == -CUDART_INF_F ? 0.f : now;
-          l *= exp2f(m - ref);
+          float fade;  // of this group's sum so far
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(fade) : "f"(m - ref));
           m = now;
+          // PAIR: the second group's first exponentials behind the first group's, and
+          // so half a tile behind from there on: their warps share the special
+          // function units, which would idle while both are at loads and maxima.
+          if (PAIR && i == 0) {
+            if (grp_w == 1) {
+              ok = wait_use(sh.mready[quad][0], u - 1);
+              if (!ok) break;
+            }
+          }
           // Weights in fp32 for the sum, rounded to bf16 for the second product
           // (a relative 2^-8 at most on each weight, what the output's own
           // rounding allows; the tensor cores take both operands in one type).
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             ps[e & 1] = add_f32x2(ps[e & 1], w);
             pk[e] = pack_bf16x2(w.x, w.y);
           }
-          l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
+          l = fmaf(l, fade, (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y));
           umma::st16_nowait(s_col, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
           umma::st16_nowait(s_col + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
           // (The first tile's P V overwrites O; rows that nobody reads move nothing.)
@@ -826,6 +836,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           umma::wait_st();
         } else if (!PAIR && lane == 0) {
           mbar_arrive(bar(sh.mready[quad][x & 1]));  // one arrival a tile, whoever reads
+        }
+        if (PAIR && i == 0 && grp_w == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sh.mready[quad][0]));
         }
         if (masked && (!PAIR || grp_w == 0)) {  // PAIR: V is mended once, and the first row tile's P V goes first
           ok = wait_use(sh.vfull[x % NV], x / NV);
@@ -880,8 +894,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       nxt = sh.pieces[u % kTreePieces];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
-      row_nxt = TreeRow{0, 0};
-      if (nxt.b >= 0) row_nxt = tree_row(p, TreeSeq{nxt.L, nxt.n, nxt.L - nxt.n}, nxt.b, node);
+      word = nxt.b >= 0 ? tree_word(p, nxt.b, nxt.n, node) : 0ull;  // used at the next turn
       if (!work) {
         if (nxt.b < 0) break;
         continue;
@@ -949,25 +962,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
 #pragma unroll 1
-        for (int e = e0; e < e0 + CH; ++e) {
-          float f[16];
-          umma::ld16(o_col + e * 16, f);
+        for (int e = e0; e < e0 + CH; e += 2) {  // 32 columns
+          uint32_t f[32];
+          umma::ld32_nowait(o_col + e * 16, f);
+          umma::wait_ld();
           if (!real) continue;
           if (whole) {
-            uint32_t o[8];
+            uint32_t o[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f[2 * j] * inv, f[2 * j + 1] * inv);
+            for (int j = 0; j < 16; ++j)
+              o[j] = pack_bf16x2(__uint_as_float(f[2 * j]) * inv, __uint_as_float(f[2 * j + 1]) * inv);
             if (sectors) {
-              st_global_32(orow + e * 16, o);
+              st_global_32(orow + e * 16, *reinterpret_cast<uint32_t(*)[8]>(&o[0]));
+              st_global_32(orow + e * 16 + 16, *reinterpret_cast<uint32_t(*)[8]>(&o[8]));
             } else {
-              reinterpret_cast<uint4*>(orow + e * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-              reinterpret_cast<uint4*>(orow + e * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                reinterpret_cast<uint4*>(orow + e * 16)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
           } else {
+            uint4* at = reinterpret_cast<uint4*>(po + (int64_t)e * 4 * row_stride * 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float4*>(po + (int64_t)(e * 4 + j) * row_stride * 4) =
-                  make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+              at[(int64_t)j * row_stride] = make_uint4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
           }
         }
         if (real && !whole && (PAIR || grp_w == 0))

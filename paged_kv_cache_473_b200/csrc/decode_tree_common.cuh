@@ -82,21 +82,26 @@ struct TreeRow {
   uint64_t nodes;
 };
 
-__device__ __forceinline__ TreeRow tree_row(const TreeParams& p, const TreeSeq& s, int b, int j) {
+// Node j's mask word as it lies in memory (0 for a node that the tree does not have).
+__device__ __forceinline__ uint64_t tree_word(const TreeParams& p, int b, int n, int j) {
+  return j < n ? (uint64_t)p.tree_mask[b * p.mask_stride + j] : 0ull;
+}
+
+__device__ __forceinline__ TreeRow tree_row(const TreeParams& p, const TreeSeq& s, int b, int j, uint64_t word) {
   TreeRow r;
   if (j >= s.n) {
     r.lo = s.base;
     r.nodes = 0;
     return r;
   }
-  const int64_t* mask = p.tree_mask + b * p.mask_stride;
-  r.nodes = (uint64_t)mask[j] & low_bits(s.n);
+  r.nodes = word & low_bits(s.n);
   r.lo = 0;
   if (p.window > 0) {
-    const int depth = tree_depth(mask, j, s.n);
+    const int depth = __popcll(r.nodes & ~(1ull << j));
     r.lo = max(0, s.base + 1 - p.window + depth);
     if (r.lo > s.base) r.lo = s.base;
     if (p.window < kMaxTreeNodes) {  // a depth is below kMaxTreeNodes: wider windows reach every node
+      const int64_t* mask = p.tree_mask + b * p.mask_stride;
       for (int i = 0; i < s.n; ++i)
         if (tree_depth(mask, i, s.n) + p.window <= depth) r.nodes &= ~(1ull << i);
     }

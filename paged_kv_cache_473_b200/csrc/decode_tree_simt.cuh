@@ -58,7 +58,10 @@ __global__ void __launch_bounds__(kTreeSimtWarps * 32, 2) decode_tree_simt_kerne
       if (r0 + i / D < all_rows) out[out_row(r0 + i / D) + i % D] = 0.f;
     return;
   }
-  if (tid < RT) row[tid] = r0 + tid < rows ? tree_row(p, s, b, (r0 + tid) / G) : TreeRow{s.base, 0};
+  if (tid < RT) {
+    const int node = r0 + tid < rows ? (r0 + tid) / G : s.n;
+    row[tid] = tree_row(p, s, b, node, tree_word(p, b, s.n, node));
+  }
   float q[RT][8], m[RT], l[RT], o[RT][8];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
