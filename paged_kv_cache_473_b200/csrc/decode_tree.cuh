@@ -790,15 +790,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           float fade;  // of this group's sum so far
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(fade) : "f"(m - ref));
           m = now;
-          // PAIR: the second group's first exponentials behind the first group's, and
-          // so half a tile behind from there on: their warps share the special
-          // function units, which would idle while both are at loads and maxima.
-          if (PAIR && i == 0) {
-            if (grp_w == 1) {
-              ok = wait_use(sh.mready[quad][0], u - 1);
-              if (!ok) break;
-            }
-          }
           // Weights in fp32 for the sum, rounded to bf16 for the second product
           // (a relative 2^-8 at most on each weight, what the output's own
           // rounding allows; the tensor cores take both operands in one type).
@@ -836,10 +827,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           umma::wait_st();
         } else if (!PAIR && lane == 0) {
           mbar_arrive(bar(sh.mready[quad][x & 1]));  // one arrival a tile, whoever reads
-        }
-        if (PAIR && i == 0 && grp_w == 0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(sh.mready[quad][0]));
         }
         if (masked && (!PAIR || grp_w == 0)) {  // PAIR: V is mended once, and the first row tile's P V goes first
           ok = wait_use(sh.vfull[x % NV], x / NV);
