@@ -35,6 +35,7 @@ struct TreeParams {
   int block_size, log2_bs, max_blocks, num_blocks;
   int log2_box;                 // rows of a K/V box: a block's, up to a tile's 64
   int window, max_context;
+  int split;                    // CTAs of a cluster that share a range (decode_tree_simt.cuh)
   int q_nodes, m_tiles;         // nodes per row tile of at most 128 query rows, row tiles of a tree_len tree
   float scale, softcap;
   int use_softcap;

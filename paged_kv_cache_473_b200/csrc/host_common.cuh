@@ -194,23 +194,35 @@ cudaError_t set_smem(Kernel k, int bytes, std::atomic<uint64_t>& done) {
 
 // Launch `kern` with cudaLaunchKernelEx; `pdl` lets it start while the
 // preceding kernel on the stream finishes (it must call griddepcontrol.wait
-// before reading that kernel's output).
+// before reading that kernel's output).  `cluster` neighbouring CTAs of the
+// grid's x form a cluster where it is above one.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, dim3 block, int smem, cudaStream_t st, bool pdl,
-                      Args&&... args) {
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, dim3 block, int smem, cudaStream_t st,
+                           bool pdl, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
   if (pdl) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
   }
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_ex(void (*kern)(KArgs...), dim3 grid, dim3 block, int smem, cudaStream_t st, bool pdl,
+                      Args&&... args) {
+  return launch_cluster(kern, grid, 1, block, smem, st, pdl, std::forward<Args>(args)...);
 }
 
 inline int sm_count() {

@@ -88,13 +88,23 @@ pa_status_t check_norm_rope(const NormRopeParams& p, int32_t num_tokens, int32_t
 // ---- tree attention -------------------------------------------------------------------
 
 template <int D>
-cudaError_t launch_tree_simt_t(const TreeParams& p, cudaStream_t st) {
-  constexpr int RT = pa::kTreeSimtRows;
-  const dim3 grid((unsigned)((p.tree_len * p.group + RT - 1) / RT), p.hkv, p.batch);
-  return launch_ex(pa::decode_tree_simt_kernel<D>, grid, dim3(pa::kTreeSimtWarps * 32), 0, st, true, p);
+cudaError_t launch_tree_simt_t(TreeParams& p, cudaStream_t st) {
+  constexpr int RT = pa::kTreeSimtRows, kWorkers = pa::kTreeSimtWarps * 32 / (D / 8);
+  const int tiles = (p.tree_len * p.group + RT - 1) / RT;
+  // Two CTAs fit on an SM: a range is split while some would have none, and every
+  // worker keeps 4 tokens.  B200, 5 nodes x 4 heads x 8 kv heads of one 776-token
+  // sequence: 20 us split in 8, 143 whole; 4 sequences of 200 tokens x 2 kv heads:
+  // 12.0 split in 4 or 8, 13.7 split to one token a worker.  Above two CTAs an SM a
+  // split loses (60 nodes x 8 heads x 4 kv heads x 2 of 822 tokens: 63 against 77 us).
+  const long long ctas = (long long)tiles * p.hkv * p.batch;
+  p.split = 1;
+  while (p.split < pa::kTreeSimtCluster && ctas * p.split < 2LL * sm_count() && p.max_context >= 8LL * p.split * kWorkers)
+    p.split *= 2;
+  return launch_cluster(pa::decode_tree_simt_kernel<D>, dim3((unsigned)(tiles * p.split), p.hkv, p.batch), p.split,
+                        dim3(pa::kTreeSimtWarps * 32), 0, st, true, p);
 }
 
-cudaError_t launch_tree_simt(const TreeParams& p, int head_dim, cudaStream_t st) {
+cudaError_t launch_tree_simt(TreeParams& p, int head_dim, cudaStream_t st) {
   switch (head_dim) {
     case 64:
       return launch_tree_simt_t<64>(p, st);
