@@ -90,7 +90,12 @@ struct TreeCfg {
   static constexpr int kBarOff = kVOff + kVStages * kKBytes;
   static constexpr int kSmemBytes = kBarOff + kSharedBytes;
   static constexpr int kRing = kKStages <= 4 ? 8 : 16;  // tiles whose rows are remembered: those loaded and not done
-  static constexpr int kLag = PAIR ? 2 : 3;             // tiles that S runs ahead of P V
+  // Tiles that S runs ahead of P V.  At most kVStages: a tile's S is done after the
+  // P V of the tile kLag before it, so a softmax warp that then mends the tile's V
+  // finds the stage's last load done, and waits for this tile's (a parity does not
+  // tell a load from the one two before it).
+  static constexpr int kLag = PAIR || kVStages < 3 ? 2 : 3;
+  static_assert(kVStages >= kLag, "V stages");
   static constexpr int kUnitCost = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // of a unit, in tiles of this head_dim (about 1.5 us)
   static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
   static constexpr int kSCol = 256;                     // four S buffers, two per group

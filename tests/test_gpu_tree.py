@@ -288,6 +288,23 @@ def test_many_short_sequences():
     assert torch.count_nonzero(_run(c, max_context_len=16)).item() == 0
 
 
+@pytest.mark.parametrize("heads,nodes", [((8, 4, 256), 44), ((8, 4, 256), 64), ((8, 4, 256), 24), ((16, 2, 256), 64),
+                                         ((32, 8, 128), 16), ((32, 8, 128), 31), ((32, 8, 128), 64), ((32, 4, 64), 8),
+                                         ((32, 4, 64), 40)])
+def test_many_tiles_in_flight(heads, nodes):
+    """Every multiprocessor goes through many units of a few tiles, the last ones
+    masked: loads, products and the mending of V at every stage of the rings."""
+    g = torch.Generator().manual_seed(nodes + heads[2])
+    for spread in ((64, 400), (250, 900)):
+        lens = torch.randint(*spread, (96,), generator=g).tolist()
+        c = _case(lens, nodes, heads, seed=32 + spread[0])
+        want = _ref(c)
+        outs = [_run(c) for _ in range(3)]
+        for out in outs:
+            ref.assert_near(out, *want, f"{heads} {nodes} {spread}")
+    assert pa.device_errors() == 0
+
+
 @pytest.mark.parametrize("heads,nodes,lens", [((32, 8, 128), 64, [5000, 70]), ((8, 4, 256), 7, [9000]),
                                               ((32, 4, 64), 24, [12345, 300, 4000]), ((1, 1, 64), 2, [20000]),
                                               ((32, 8, 128), 1, [64 * 200 + 1])])
