@@ -36,7 +36,10 @@
 // issue, and the load of a piece's Q as soon as the last S of the piece before
 // is done.  Warp 9: the schedule (pieces go to the other warps through a ring in
 // shared memory) and the TMA loads of K; warp 10: those of V (boxes of 64 columns and
-// as many rows as lie together, a block's up to 64, all issued by one lane).
+// as many rows as lie together, a block's up to 64, all issued by one lane).  Warp
+// 11: the mending of V in masked tiles, between its load and its product (by the
+// softmax warps, which then waited for V three tiles early, a masked tile took
+// twice as long).
 // Every wait is bounded; a wait that gives up raises the abort flag, which ends all
 // roles.
 //
@@ -59,7 +62,7 @@ namespace pa {
 
 constexpr int kTreeRows = 128;  // query rows per row tile (UMMA M)
 constexpr int kTreeTile = 64;   // keys per tile
-constexpr int kTreeWarps = 11;
+constexpr int kTreeWarps = 12;
 constexpr int kTreeThreads = kTreeWarps * 32;
 constexpr int kTreeCombineRows = 8;
 constexpr int kTreeMinTiles = 2;    // shortest range: below, a piece's fixed cost outweighs its tiles
@@ -69,6 +72,7 @@ constexpr int kTreeClaimTiles = 48;
 constexpr int kTreeClaimsPerCta = 2;
 constexpr int kTreeMaxPairs = 4;    // 512 rows in row tiles of one: counters in use
 constexpr int kTreePieces = 4;      // ring of pieces between the roles
+constexpr int kTreeMarks = 2 * kTreePieces;  // pieces whose marks of V are kept: those between the mender and the last epilogue
 
 // QR: rows of Q that shared memory holds (64 or 128).
 template <int D, int QR, bool PAIR>
@@ -80,7 +84,7 @@ struct TreeCfg {
   static constexpr int kKVPanelBytes = kTreeTile * 128;
   static constexpr int kKBytes = kPanels * kKVPanelBytes;
   static constexpr int kMaxSmem = 232448;
-  static constexpr int kSharedBytes = D <= 128 ? 4096 : 3072;
+  static constexpr int kSharedBytes = D == 256 && QR == 64 ? 3072 : 4096;
   static constexpr int kFit = (kMaxSmem - kSharedBytes - kRowTiles * kQBytes) / kKBytes;
   static constexpr int kKStages = (kFit + 1) / 2 < 10 ? (kFit + 1) / 2 : 10;
   static constexpr int kVStages = kFit / 2 < 10 ? kFit / 2 : 10;
@@ -90,12 +94,9 @@ struct TreeCfg {
   static constexpr int kBarOff = kVOff + kVStages * kKBytes;
   static constexpr int kSmemBytes = kBarOff + kSharedBytes;
   static constexpr int kRing = kKStages <= 4 ? 8 : 16;  // tiles whose rows are remembered: those loaded and not done
-  // Tiles that S runs ahead of P V.  At most kVStages: a tile's S is done after the
-  // P V of the tile kLag before it, so a softmax warp that then mends the tile's V
-  // finds the stage's last load done, and waits for this tile's (a parity does not
-  // tell a load from the one two before it).
+  // Tiles that S runs ahead of P V (three with two stages of V: 61.4 for 58.7 us on
+  // 121 trees of 44 nodes, head_dim 256).
   static constexpr int kLag = PAIR || kVStages < 3 ? 2 : 3;
-  static_assert(kVStages >= kLag, "V stages");
   static constexpr int kUnitCost = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // of a unit, in tiles of this head_dim (about 1.5 us)
   static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
   static constexpr int kSCol = 256;                     // four S buffers, two per group
@@ -114,13 +115,13 @@ struct TreePiece {
 template <int D, int QR, bool PAIR>
 struct TreeShared {
   using C = TreeCfg<D, QR, PAIR>;
-  uint64_t kfull[C::kKStages], kempty[C::kKStages], vfull[C::kVStages], vempty[C::kVStages];
+  uint64_t kfull[C::kKStages], kempty[C::kKStages], vfull[C::kVStages], vready[C::kVStages], vempty[C::kVStages];
   uint64_t sfull[2][2], pready[2][2], odone[2][2];  // [group][buffer]
   uint64_t mready[4][2];                            // [warp of the group][tile parity]
   uint64_t pfull[kTreePieces], pempty[kTreePieces];
   uint64_t rfull[C::kRing];                         // rows[] of a tile are written
   uint64_t qfull, epi, ofree, drain;
-  uint64_t bad[3][4];  // by piece: rows of V with elements that are not finite, in each masked tile
+  uint64_t bad[kTreeMarks][4];  // by piece: rows of V with elements that are not finite, in each masked tile
   TreePiece pieces[kTreePieces];
   alignas(16) int rows[C::kRing][4];  // by tile: cache rows of its boxes (-1: not loaded; -2: no more tiles)
   uint8_t skip[C::kRing];  // by tile: 16-row slices whose block id is bad
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto bar = [&](const uint64_t& b) { return smem_addr(&b); };
   if (tid == 0) {
     for (int s = 0; s < NK; ++s) mbar_init(bar(sh.kfull[s]), 1), mbar_init(bar(sh.kempty[s]), 1);
-    for (int s = 0; s < NV; ++s) mbar_init(bar(sh.vfull[s]), 1), mbar_init(bar(sh.vempty[s]), 1);
+    for (int s = 0; s < NV; ++s) mbar_init(bar(sh.vfull[s]), 1), mbar_init(bar(sh.vready[s]), 1), mbar_init(bar(sh.vempty[s]), 1);
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(sh.sfull[s >> 1][s & 1]), 1);
       mbar_init(bar(sh.pready[s >> 1][s & 1]), 4);
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int s = 0; s < kTreePieces; ++s) {
       mbar_init(bar(sh.pfull[s]), 1);
-      mbar_init(bar(sh.pempty[s]), 9);  // the MMA warp and the softmax warps
+      mbar_init(bar(sh.pempty[s]), 10);  // the MMA warp, the mending warp and the softmax warps
     }
     for (int s = 0; s < C::kRing; ++s) mbar_init(bar(sh.rfull[s]), 1);
     mbar_init(bar(sh.qfull), 1);
@@ -341,7 +342,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
-  if (tid < 12) sh.bad[tid / 4][tid % 4] = 0;
   if (warp == 0) umma::alloc(smem_addr(&sh.tmem), 512);
   pdl_wait();  // a programmatic dependent: nothing of global memory was touched before
   long long before, all;
@@ -525,6 +525,101 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           (void)mbar_wait_bounded(bar(sh.vfull[j % NV]), (j / NV) & 1, kDrainLimitNs);
       }
     }
+  } else if (warp == 11) {
+    // ================= mending of V =================
+    // Every tile of V passes through here between its load and its product.  Most
+    // pass as they are.
+    bool ok = true;
+    int x = 0;
+    for (int u = 0; ok && !*abort_flag; ++u) {
+      ok = wait_use(sh.pfull[u % kTreePieces], u / kTreePieces);
+      if (!ok) break;
+      const TreePiece c = sh.pieces[u % kTreePieces];
+      uint64_t* bad = sh.bad[u % kTreeMarks];
+      if (lane < 4) bad[lane] = 0;  // every warp is past the piece kTreeMarks ago
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.pempty[u % kTreePieces]));
+      if (c.b < 0) break;
+      const int base = c.L - c.n, kt0 = c.ulo & ~(TILE - 1);
+      const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;  // rows' windows start before it
+      for (int i = c.t0; i < c.t1; ++i, ++x) {
+        ok = wait_use(sh.vfull[x % NV], x / NV);
+        if (!ok) break;
+        const int kt = kt0 + i * TILE;
+        const uint32_t skip = *const_cast<volatile uint8_t*>(&sh.skip[x % C::kRing]);
+        if (kt < w_end || kt + TILE > base || kt < c.ulo || skip != 0) {
+          constexpr int CPR = C::kPanels * 8, RPI = 32 / CPR, UNROLL = 8;  // 16-byte chunks of a row, rows at a time
+          const uint32_t vst = v_s + (x % NV) * C::kKBytes;
+          // Rows of V that no row attends (they were not loaded, or hold what
+          // stands behind the end): zero.  Rows that some may attend and some
+          // not, the tree's and those at the windows' starts: see above.
+          uint64_t none = low_bits(min(max(c.ulo - kt, 0), TILE)) | ~low_bits(min(max(c.L - kt, 0), TILE));
+          for (int e = 0; e < 4; ++e)
+            if ((skip >> e) & 1u) none |= 0xffffull << (16 * e);
+          const bool tree = kt + TILE > base;
+          uint64_t some = tree ? ~low_bits(max(base - kt, 0)) : 0ull;
+          if (kt < w_end) some |= low_bits(min(w_end - kt, TILE));
+          some &= ~none;
+          const int slot = tree ? 2 + (kt - (base & ~(TILE - 1))) / TILE : i;
+          auto chunk = [&](int at) {  // this lane's of row `at`
+            return vst + (lane % CPR >> 3) * C::kKVPanelBytes + at * 128 + ((lane & 7) << 4);
+          };
+#pragma unroll 1
+          for (int from = 0; from < TILE; from += UNROLL * RPI) {
+            const uint64_t some_here = (some >> from) & low_bits(UNROLL * RPI);
+            if (some_here) {
+              uint32_t v[UNROLL][4], seen = 0;
+#pragma unroll
+              for (int j = 0; j < UNROLL; ++j) {
+                const int at = from + j * RPI + lane / CPR;
+                v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
+                if ((some >> at) & 1ull)
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(v[j][0]), "=r"(v[j][1]), "=r"(v[j][2]), "=r"(v[j][3])
+                               : "r"(chunk(at)));
+              }
+              // Exponent bits all set (not finite): 0x7f80 and above without the sign.
+#pragma unroll
+              for (int j = 0; j < UNROLL; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) seen |= (v[j][k] & 0x7fff7fffu) + 0x00800080u;
+              if (seen & 0x80008000u) {
+#pragma unroll 1
+                for (int j = 0; j < UNROLL; ++j) {
+                  const int at = from + j * RPI + lane / CPR;
+                  if (!((some >> at) & 1ull)) continue;
+                  bool change = false;
+#pragma unroll 1
+                  for (int k = 0; k < 4; ++k) {
+                    uint32_t w;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(chunk(at) + 4 * k));
+                    uint32_t keep = w;
+                    if ((w & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                    if ((w & 0x7f800000u) == 0x7f800000u) keep &= 0xffffu;
+                    if (keep == w) continue;
+                    change = true;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(chunk(at) + 4 * k), "r"(keep) : "memory");
+                  }
+                  if (change) atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << at);
+                }
+              }
+            }
+            if ((none >> from) & low_bits(UNROLL * RPI)) {
+#pragma unroll
+              for (int j = 0; j < UNROLL; ++j) {
+                const int at = from + j * RPI + lane / CPR;
+                if ((none >> at) & 1ull)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(at)), "r"(0) : "memory");
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();  // visible to the tensor core's reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.vready[x % NV]));
+      }
+    }
+    if (!ok) give_up();
   } else if (warp == 8) {
     // ================= MMA issuer (one elected lane, from here to the end) =================
     // Everything this lane does between two products delays the next one, so
@@ -535,7 +630,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // Descriptors of the first Q, K and V bytes; the others lie (bytes / 16) on.
       const uint64_t q_desc = umma::desc_sw128(q_s, 16, 1024), k_desc = umma::desc_sw128(k_s, 16, 1024);
       const uint64_t v_desc = umma::desc_sw128(v_s, C::kKVPanelBytes, 1024);
-      const uint32_t kfull = bar(sh.kfull[0]), kempty = bar(sh.kempty[0]), vfull = bar(sh.vfull[0]);
+      const uint32_t kfull = bar(sh.kfull[0]), kempty = bar(sh.kempty[0]), vready = bar(sh.vready[0]);
       const uint32_t vempty = bar(sh.vempty[0]), sfull = bar(sh.sfull[0][0]), pready = bar(sh.pready[0][0]);
       const uint32_t odone = bar(sh.odone[0][0]);
       auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_bounded(b, parity, kWaitLimitNs); };
@@ -579,7 +674,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const bool s = i < len, o = i >= LAG;
           if (o) {
             if (i == LAG && u > 0) ok = wait(bar(sh.ofree), (u - 1) & 1);  // the last piece's O is read
-            ok = ok && wait(vfull + 8 * vst, vph);
+            ok = ok && wait(vready + 8 * vst, vph);
           }
           if (s) ok = ok && (i > 0 || wait(bar(sh.qfull), u & 1)) && wait(kfull + 8 * kst, kph);
           else if (asked == u + 1) (void)ask(false);
@@ -686,7 +781,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const TreeRow row = work ? tree_row(p, TreeSeq{L, c.n, base}, c.b, node, word) : TreeRow{0, 0};
       // Rows' windows start in [ulo, ulo + 63] (a depth is at most 63) and at most at base.
       const int w_end = p.window > 0 ? min(base, c.ulo + TILE - 1) : 0;
-      uint64_t* bad = sh.bad[(u + 2) % 3];  // piece u - 1's
+      const uint64_t* bad = sh.bad[(u + kTreeMarks - 1) % kTreeMarks];  // piece u - 1's
       float m = -CUDART_INF_F, l = 0.f;  // this group's last reference, its sum
       for (int i = PAIR ? 0 : (x0 + grp_w) & 1; i < len; i += PAIR ? 1 : 2) {
         const int x = x0 + i, k = count_of(x);
@@ -833,48 +928,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         } else if (!PAIR && lane == 0) {
           mbar_arrive(bar(sh.mready[quad][x & 1]));  // one arrival a tile, whoever reads
         }
-        if (masked && (!PAIR || grp_w == 0)) {  // PAIR: V is mended once, and the first row tile's P V goes first
-          ok = wait_use(sh.vfull[x % NV], x / NV);
-          if (!ok) break;
-          const uint32_t vst = v_s + (x % NV) * C::kKBytes;
-          constexpr int CPR = C::kPanels * 8;  // 16-byte chunks of a row
-          const int me = tid & 127;
-          // Rows of V that no row attends (they were not loaded, or hold what
-          // stands behind the end): zero.  Rows that some may attend and some
-          // not, the tree's and those at the windows' starts: see above.
-          uint64_t none = low_bits(min(max(c.ulo - kt, 0), TILE)) | ~low_bits(min(max(L - kt, 0), TILE));
-          for (int e = 0; e < 4; ++e)
-            if ((skip >> e) & 1u) none |= 0xffffull << (16 * e);
-          const bool tree = kt + TILE > base;
-          uint64_t some = tree ? ~low_bits(max(base - kt, 0)) : 0ull;
-          if (kt < w_end) some |= low_bits(min(w_end - kt, TILE));
-          some &= ~none;
-          const int slot = tree ? 2 + (kt - (base & ~(TILE - 1))) / TILE : (kt - kt0) / TILE;
-          constexpr int RPI = 128 / CPR;  // rows at a time
-#pragma unroll 1
-          for (int at = me / CPR; at < TILE; at += RPI) {
-            if (!(((none | some) >> at) & 1ull)) continue;
-            const uint32_t dst = vst + (me % CPR >> 3) * C::kKVPanelBytes + at * 128 + ((me & 7) << 4);
-            uint32_t v[4] = {0, 0, 0, 0};
-            bool change = (none >> at) & 1ull;
-            if (!change) {
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                           : "r"(dst));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {  // exponent bits all set: not finite
-                if ((v[j] & 0x7f80u) == 0x7f80u) v[j] &= 0xffff0000u, change = true;
-                if ((v[j] & 0x7f800000u) == 0x7f800000u) v[j] &= 0xffffu, change = true;
-              }
-              if (change) atomicOr(reinterpret_cast<unsigned long long*>(&bad[slot]), 1ull << at);
-            }
-            if (change)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                           "r"(v[3])
-                           : "memory");
-          }
-          fence_proxy_async_smem();  // visible to the tensor core's reads
-        }
         umma::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.pready[grp_w][k & 1]));
@@ -906,9 +959,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!ok) break;
       umma::fence_after();
       if (!PAIR && active) sh.l[grp_w][r] = l;
-      // The next piece's marks, clear before any warp can be at that piece and
-      // after every warp is past the piece that used them (three ago).
-      if (tid < 4) sh.bad[u % 3][tid] = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.epi));
       ok = wait_use(sh.epi, u - 1);
@@ -916,7 +966,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!PAIR && active) l = sh.l[0][r] + sh.l[1][r];
       uint64_t marks = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) marks |= *const_cast<volatile uint64_t*>(&bad[e]);
+      for (int e = 0; e < 4; ++e) marks |= *const_cast<const volatile uint64_t*>(&bad[e]);
       const bool begins = c.t0 == 0, whole = begins && c.t1 == c.tiles;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t slot = ((int64_t)c.range * p.m_tiles + mt) * 2 + (begins ? 1 : 0);
