@@ -64,7 +64,7 @@ constexpr int kTreeRows = 128;  // query rows per row tile (UMMA M)
 constexpr int kTreeTile = 64;   // keys per tile
 constexpr int kTreeWarps = 12;
 constexpr int kTreeThreads = kTreeWarps * 32;
-constexpr int kTreeCombineRows = 8;
+constexpr int kTreeCombineRows = 8;  // rows of the partials that lie side by side
 constexpr int kTreeMinTiles = 2;    // shortest range: below, a piece's fixed cost outweighs its tiles
 // Claimed ranges: the last 3/16 of the line in up to two per CTA, where a CTA's
 // share is at least kTreeClaimTiles tiles (a shorter share is all one range).
@@ -1052,42 +1052,72 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // and row tile t: the unit whose first piece is in c (slot 1) and that goes on;
 // the other pieces are in slot 0 of the next ranges.  With M = max m_p:
 //   out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,
-// in piece order.  blockIdx.y: 8 rows; a thread has four columns of one row,
-// and neighbouring threads neighbouring rows, as the partials lie.
-template <int D>
+// in piece order.  blockIdx.y: 8 EACH rows; a thread has four columns of EACH of
+// them, and neighbouring threads neighbouring rows, as the partials lie.  M runs
+// along, so that no load waits for another.
+template <int D, int EACH>
 __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p) {
+  constexpr int kRows = kTreeCombineRows;
   pdl_wait();  // the partials come from the attention grid
   const int c = blockIdx.x / p.m_tiles, t = blockIdx.x - c * p.m_tiles;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kTreeMaxPairs) p.queue[threadIdx.x] = 0;  // for the next call
   const int ranges = p.ws_rec[-1].x;
   const int4 rec = p.ws_rec[blockIdx.x];
   if (c >= ranges || rec.x < 2 || c + rec.x > ranges) return;
-  const int G = p.group, r = blockIdx.y * kTreeCombineRows + (threadIdx.x & (kTreeCombineRows - 1));
-  const int node = t * p.q_nodes + r / G;
-  if (r >= p.q_nodes * G || node >= min(rec.w, p.tree_len)) return;
   if ((unsigned)rec.y >= (unsigned)p.batch || (unsigned)rec.z >= (unsigned)p.hkv) return;  // left by a call that gave up
-  const int col4 = threadIdx.x / kTreeCombineRows, row_stride = tree_row_stride(p);
+  const int G = p.group, row_stride = tree_row_stride(p);
+  const int r0 = blockIdx.y * EACH * kRows + (threadIdx.x & (kRows - 1)), col4 = threadIdx.x / kRows;
+  const int rows = min(p.q_nodes, min(rec.w, p.tree_len) - t * p.q_nodes) * G;  // the unit's in this row tile
+  if (r0 >= rows) return;
   auto slot = [&](int k) { return ((int64_t)(c + k) * p.m_tiles + t) * 2 + (k == 0 ? 1 : 0); };
-  float M = -CUDART_INF_F;
-  for (int k = 0; k < rec.x; ++k) M = fmaxf(M, p.ws_ml[(slot(k) * row_stride + r) * 2]);
-  const float ref = M == -CUDART_INF_F ? 0.f : M;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < rec.x; ++k) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (slot(k) * row_stride + r) * 2);
-    const float4 o = *reinterpret_cast<const float4*>(p.ws_o + (slot(k) * (D / 4) + col4) * row_stride * 4 + r * 4);
-    const float w = exp2f(ml.x - ref);
-    den = fmaf(w, ml.y, den);
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+  float M[EACH], den[EACH];
+  float4 acc[EACH];
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    M[j] = -CUDART_INF_F;
+    den[j] = 0.f;
+    acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;  // a row that attends nothing is zero
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                       (((int64_t)rec.y * p.tree_len + node) * p.hq + (int64_t)rec.z * G + r % G) * D + col4 * 4;
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  for (int k0 = 0; k0 < rec.x; k0 += 2) {
+    float2 ml[2][EACH];
+    float4 o[2][EACH];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < EACH; ++j) {
+        const int r = r0 + j * kRows;
+        ml[k][j] = make_float2(-CUDART_INF_F, 0.f);
+        o[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && k0 + k < rec.x) {
+          const int64_t at = slot(k0 + k);
+          ml[k][j] = *reinterpret_cast<const float2*>(p.ws_ml + (at * row_stride + r) * 2);
+          o[k][j] = *reinterpret_cast<const float4*>(p.ws_o + (at * (D / 4) + col4) * row_stride * 4 + r * 4);
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < EACH; ++j) {
+        const float top = fmaxf(M[j], ml[k][j].x), ref = top == -CUDART_INF_F ? 0.f : top;
+        const float old = exp2f(M[j] - ref), w = exp2f(ml[k][j].x - ref);
+        M[j] = top;
+        den[j] = fmaf(w, ml[k][j].y, old * den[j]);
+        acc[j].x = fmaf(w, o[k][j].x, old * acc[j].x);
+        acc[j].y = fmaf(w, o[k][j].y, old * acc[j].y);
+        acc[j].z = fmaf(w, o[k][j].z, old * acc[j].z);
+        acc[j].w = fmaf(w, o[k][j].w, old * acc[j].w);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    const int r = r0 + j * kRows;
+    if (r >= rows) continue;
+    const float inv = den[j] > 0.f ? 1.f / den[j] : 0.f;  // a row that attends nothing is zero
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + col4 * 4 +
+                         (((int64_t)rec.y * p.tree_len + t * p.q_nodes + r / G) * p.hq + (int64_t)rec.z * G + r % G) * D;
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+  }
 }
 
 }  // namespace pa

@@ -167,8 +167,18 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t s
   if (e != cudaSuccess) return e;
   e = launch_ex(kern, dim3(w.grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  return launch_ex(pa::tree_combine_kernel<D>, dim3(w.records, w.rows / pa::kTreeCombineRows), dim3(2 * D), 0, st,
-                   true, p);
+  // Records that the call can have (no range is claimed where no share can be
+  // long enough for it), 8 of their rows a block, or 32 where that would be more
+  // than two waves of blocks.  B200: 7 trees of 39 nodes 32.2 us with 8 rows of
+  // every record there might be, 25.8 so; 64 trees of 8 nodes 26.4 with 8 rows, 32.1 with 32.
+  const int groups = w.records / w.m_tiles / (1 + pa::kTreeClaimsPerCta);
+  const long long longest = std::min<long long>(p.max_context, (long long)p.max_blocks * p.block_size);
+  const long long line = (long long)p.batch * p.hkv * (longest / pa::kTreeTile + 2 + Cfg::kUnitCost);
+  const int ranges = line / groups + 1 < pa::kTreeClaimTiles ? groups : groups * (1 + pa::kTreeClaimsPerCta);
+  const int row_blocks = w.rows / pa::kTreeCombineRows;
+  const bool many = 2LL * D * ranges * w.m_tiles * row_blocks > 2 * 2048LL * sm_count();
+  const dim3 grid(ranges * w.m_tiles, many ? (row_blocks + 3) / 4 : row_blocks);
+  return launch_ex(many ? pa::tree_combine_kernel<D, 4> : pa::tree_combine_kernel<D, 1>, grid, dim3(2 * D), 0, st, true, p);
 }
 
 cudaError_t launch_tree(const TreeParams& p, int head_dim, const TreePlan& w, cudaStream_t st) {
