@@ -32,12 +32,12 @@
 // the one that goes on in the next), and joined by tree_combine_kernel.  Which CTA
 // takes a range changes no bit of the result.
 //
-// Warps 0-7: softmax, one row per thread; they also write the rows.  Warp 8: MMA
+// Warps 0-7: softmax, one row per thread; they also write the rows.  Warp 11: MMA
 // issue, and the load of a piece's Q as soon as the last S of the piece before
-// is done.  Warp 9: the schedule (pieces go to the other warps through a ring in
-// shared memory) and the TMA loads of K; warp 10: those of V (boxes of 64 columns and
+// is done.  Warp 10: the schedule (pieces go to the other warps through a ring in
+// shared memory) and the TMA loads of K; warp 9: those of V (boxes of 64 columns and
 // as many rows as lie together, a block's up to 64, all issued by one lane).  Warp
-// 11: the mending of V in masked tiles, between its load and its product (by the
+// 8: the mending of V in masked tiles, between its load and its product (by the
 // softmax warps, which then waited for V three tiles early, a masked tile took
 // twice as long).
 // Every wait is bounded; a wait that gives up raises the abort flag, which ends all
@@ -64,6 +64,11 @@ constexpr int kTreeRows = 128;  // query rows per row tile (UMMA M)
 constexpr int kTreeTile = 64;   // keys per tile
 constexpr int kTreeWarps = 12;
 constexpr int kTreeThreads = kTreeWarps * 32;
+// The warps behind the eight of the softmax.  Warps w and w + 4 share a scheduler, and
+// row tiles of up to 64 rows leave the last two schedulers without softmax: there
+// the two warps that pace the others (B200: 128 trees of 16 nodes 242 us with
+// these roles the other way round, 227 so; 7 of 39 nodes 30.5 and 29.3).
+constexpr int kTreeMendWarp = 8, kTreeVWarp = 9, kTreeKWarp = 10, kTreeMmaWarp = 11;
 constexpr int kTreeCombineRows = 8;  // rows of the partials that lie side by side
 constexpr int kTreeMinTiles = 2;    // shortest range: below, a piece's fixed cost outweighs its tiles
 // Claimed ranges: the last 3/16 of the line in up to two per CTA, where a CTA's
@@ -380,7 +385,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto group_of = [&](int x) { return PAIR ? 0 : x & 1; };
   auto count_of = [&](int x) { return PAIR ? x : x >> 1; };
 
-  if (warp == 9) {
+  if (warp == kTreeKWarp) {
     // ================= schedule, TMA loads of K =================
     // Block ids of a piece's boxes come in windows of 32, lane l holding box
     // wb + l (pages) and wb + 32 + l (pages2); the next piece, and the block ids
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int j = max(issued - NK, 0); j < issued; ++j)
         (void)mbar_wait_bounded(bar(sh.kfull[j % NK]), (j / NK) & 1, kDrainLimitNs);
     }
-  } else if (warp == 10) {
+  } else if (warp == kTreeVWarp) {
     // ================= TMA loads of V (one elected lane) =================
     if (umma::elect()) {
       const int box_rows = 1 << p.log2_box;
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           (void)mbar_wait_bounded(bar(sh.vfull[j % NV]), (j / NV) & 1, kDrainLimitNs);
       }
     }
-  } else if (warp == 11) {
+  } else if (warp == kTreeMendWarp) {
     // ================= mending of V =================
     // Every tile of V passes through here between its load and its product.  Most
     // pass as they are.
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
     }
     if (!ok) give_up();
-  } else if (warp == 8) {
+  } else if (warp == kTreeMmaWarp) {
     // ================= MMA issuer (one elected lane, from here to the end) =================
     // Everything this lane does between two products delays the next one, so
     // stages and parities are counted up, not divided out of a tile's number.
