@@ -21,9 +21,13 @@
 // held by D / 8 neighbouring lanes, each with four pairs: two chunks of four
 // elements (8-byte accesses for bf16), so that nothing but the norm's sum
 // passes between lanes, and a lane reads and writes only its own elements
-// (which makes in-place calls safe).  (With eight neighbouring elements a lane and
-// the pairs' other halves by shuffles, 16384 tokens of 48 rows of 128 took 83 us
-// instead of 74, 0.83 of the copy rate; with 4 or 10 CTAs an SM 83 and 104.)  The token's rotary / 2 angles are computed once, two or so a
+// (which makes in-place calls safe).  Issue slots come next to DRAM (72 % of them
+// used before the arithmetic was packed), so it goes two elements to an instruction.
+// B200, 16384 tokens of 48 rows of 128, bf16: 68 us, 0.90 of the copy rate; 74
+// one element at a time; with 6, 9 or 10 CTAs an SM 72, 70 and 78; three rows in
+// flight 71, six (at 6 CTAs) 69; the sums of four rows taken together, with fewer shuffles, 84 (a
+// row then waits for the others); before, with eight neighbouring elements a lane and the
+// pairs' other halves by shuffles, 83.  The token's rotary / 2 angles are computed once, two or so a
 // lane, and pass through shared memory; a lane sits at the same place of each
 // of its rows and keeps the four it needs in registers.
 #pragma once
@@ -54,6 +58,11 @@ struct NormRopeParams {
 
 constexpr int kNormRopeWarps = 4;
 
+// Four consecutive elements in fp32, in pairs for packed arithmetic.
+struct Wide4 {
+  float2 a, b;
+};
+
 // Four consecutive elements, as they lie in memory.
 template <typename T>
 struct Raw4;
@@ -62,9 +71,11 @@ struct Raw4<__nv_bfloat16> {
   uint2 a;
   __device__ __forceinline__ void load(const void* src) { a = *static_cast<const uint2*>(src); }
   __device__ __forceinline__ void store(void* dst) const { *static_cast<uint2*>(dst) = a; }
-  __device__ __forceinline__ float4 wide() const { return make_float4(bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y)); }
-  __device__ __forceinline__ void round(float4 x) {  // to nearest even
-    a = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  __device__ __forceinline__ Wide4 wide() const {
+    return {make_float2(bf16_lo(a.x), bf16_hi(a.x)), make_float2(bf16_lo(a.y), bf16_hi(a.y))};
+  }
+  __device__ __forceinline__ void round(Wide4 x) {  // to nearest even
+    a = make_uint2(pack_bf16x2(x.a.x, x.a.y), pack_bf16x2(x.b.x, x.b.y));
   }
 };
 template <>
@@ -72,24 +83,25 @@ struct Raw4<float> {
   float4 a;
   __device__ __forceinline__ void load(const void* src) { a = *static_cast<const float4*>(src); }
   __device__ __forceinline__ void store(void* dst) const { *static_cast<float4*>(dst) = a; }
-  __device__ __forceinline__ float4 wide() const { return a; }
-  __device__ __forceinline__ void round(float4 x) { a = x; }
+  __device__ __forceinline__ Wide4 wide() const { return {make_float2(a.x, a.y), make_float2(a.z, a.w)}; }
+  __device__ __forceinline__ void round(Wide4 x) { a = make_float4(x.a.x, x.a.y, x.b.x, x.b.y); }
 };
 
-__device__ __forceinline__ float4 scale4(float4 x, float s, float4 w) {
-  return make_float4(x.x * s * w.x, x.y * s * w.y, x.z * s * w.z, x.w * s * w.w);
+__device__ __forceinline__ Wide4 wide4(const float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(x);
+  return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+__device__ __forceinline__ Wide4 scale4(Wide4 x, float s, Wide4 w) {
+  const float2 s2 = make_float2(s, s);
+  return {mul_f32x2(mul_f32x2(x.a, s2), w.a), mul_f32x2(mul_f32x2(x.b, s2), w.b)};
 }
-// a cos - b sin, b cos + a sin.
-__device__ __forceinline__ float4 turn4(float4 a, float4 b, float4 c, float4 s) {
-  return make_float4(fmaf(-b.x, s.x, a.x * c.x), fmaf(-b.y, s.y, a.y * c.y), fmaf(-b.z, s.z, a.z * c.z),
-                     fmaf(-b.w, s.w, a.w * c.w));
+// x u + y v.
+__device__ __forceinline__ Wide4 turn4(Wide4 x, Wide4 u, Wide4 y, Wide4 v) {
+  return {fma_f32x2(y.a, v.a, mul_f32x2(x.a, u.a)), fma_f32x2(y.b, v.b, mul_f32x2(x.b, u.b))};
 }
-__device__ __forceinline__ float4 back4(float4 a, float4 b, float4 c, float4 s) {
-  return make_float4(fmaf(a.x, s.x, b.x * c.x), fmaf(a.y, s.y, b.y * c.y), fmaf(a.z, s.z, b.z * c.z),
-                     fmaf(a.w, s.w, b.w * c.w));
+// (a cos - b sin, b cos + a sin) of a pair in (x, y).
+__device__ __forceinline__ float2 turn_pair(float2 x, float c, float s) {
+  return make_float2(fmaf(-x.y, s, x.x * c), fmaf(x.x, s, x.y * c));
 }
 
 template <typename T, int D, bool APPEND>
@@ -160,11 +172,14 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const
   };
 
   // This lane's angles: four pairs, or (interleaved) two pairs' in each chunk, both elements' the same.
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+  Wide4 c = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   if (rotated) {  // half-split: pair 4 ch + e; interleaved: chunk elements (2 e, 2 e + 1) are pair 4 ch + e
-    c = *reinterpret_cast<const float4*>(&cosines[warp][ch * 4]);
-    sn = *reinterpret_cast<const float4*>(&sines[warp][ch * 4]);
+    c = wide4(&cosines[warp][ch * 4]);
+    sn = wide4(&sines[warp][ch * 4]);
   }
+  const Wide4 minus = {make_float2(-sn.a.x, -sn.a.y), make_float2(-sn.b.x, -sn.b.y)};
+  const int turned_rows = p.hq + p.hkv;  // of q and k; v rows are copied as they are
+  const bool normed = p.q_weight || p.k_weight;
 
   for (int r0 = begin; r0 < end; r0 += U * RPW) {
 #pragma unroll
@@ -172,34 +187,35 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const
       const int first = r0 + u * RPW, r = first + mine;  // `first`: the same in all lanes
       if (first >= end) break;
       const bool real = r < end;
-      if (first < p.hq + p.hkv) {  // some row is of q or k; v rows are copied as they are
-        const bool turned = r < p.hq + p.hkv;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (first < turned_rows) {
+        const bool turned = r < turned_rows;
+        Wide4 x = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, y = x;
         if (real) x = a[u].wide(), y = b[u].wide();
-        if (p.q_weight || p.k_weight) {
-          float ss = dot4(x, x) + dot4(y, y);
+        if (normed) {
+          const float2 t = fma_f32x2(x.a, x.a, fma_f32x2(x.b, x.b, fma_f32x2(y.a, y.a, mul_f32x2(y.b, y.b))));
+          float ss = t.x + t.y;
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
           const float* w = r < p.hq ? p.q_weight : p.k_weight;
           if (turned && w) {
-            const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-            x = scale4(x, inv, *reinterpret_cast<const float4*>(w + lo));
-            y = scale4(y, inv, *reinterpret_cast<const float4*>(w + hi));
+            const float inv = rsqrtf(ss * (1.f / D) + p.eps);  // within 2 units of the last place
+            x = scale4(x, inv, wide4(w + lo));
+            y = scale4(y, inv, wide4(w + hi));
           }
         }
-        float4 xr, yr;
-        if (p.interleaved) {
-          xr = make_float4(fmaf(-x.y, sn.x, x.x * c.x), fmaf(x.x, sn.x, x.y * c.x), fmaf(-x.w, sn.y, x.z * c.y),
-                           fmaf(x.z, sn.y, x.w * c.y));
-          yr = make_float4(fmaf(-y.y, sn.z, y.x * c.z), fmaf(y.x, sn.z, y.y * c.z), fmaf(-y.w, sn.w, y.z * c.w),
-                           fmaf(y.z, sn.w, y.w * c.w));
-        } else {
-          xr = turn4(x, y, c, sn);
-          yr = back4(x, y, c, sn);
-        }
-        if (turned) {  // (not rotated: as it is, since 0 times an infinity is not nothing)
-          a[u].round(rotated ? xr : x);
-          b[u].round(rotated ? yr : y);
+        if (turned) {
+          if (rotated) {  // (not rotated: as it is, since 0 times an infinity is not nothing)
+            if (p.interleaved) {
+              x = {turn_pair(x.a, c.a.x, sn.a.x), turn_pair(x.b, c.a.y, sn.a.y)};
+              y = {turn_pair(y.a, c.b.x, sn.b.x), turn_pair(y.b, c.b.y, sn.b.y)};
+            } else {
+              const Wide4 z = turn4(x, c, y, minus);
+              y = turn4(y, c, x, sn);
+              x = z;
+            }
+          }
+          a[u].round(x);
+          b[u].round(y);
         }
       }
       if (real && (in_pool || r < p.hq)) {
