@@ -23,13 +23,13 @@
 // passes between lanes, and a lane reads and writes only its own elements
 // (which makes in-place calls safe).  Issue slots come next to DRAM (72 % of them
 // used before the arithmetic was packed), so it goes two elements to an instruction.
-// B200, 16384 tokens of 48 rows of 128, bf16: 68 us, 0.90 of the copy rate; 74
-// one element at a time; with 6, 9 or 10 CTAs an SM 72, 70 and 78; three rows in
-// flight 71, six (at 6 CTAs) 69; the sums of four rows taken together, with fewer shuffles, 84 (a
-// row then waits for the others); before, with eight neighbouring elements a lane and the
-// pairs' other halves by shuffles, 83.  The token's rotary / 2 angles are computed once, two or so a
-// lane, and pass through shared memory; a lane sits at the same place of each
-// of its rows and keeps the four it needs in registers.
+// B200, append of 16384 tokens of 48 rows of 128, bf16: 68 us, 0.90 of the copy rate;
+// 74 one element at a time; with 6, 9 or 10 CTAs an SM 72, 70 and 78; three rows in
+// flight 71, six (at 6 CTAs) 69; the sums of four rows taken together, with fewer
+// shuffles, 84 (a row then waits for the others); with eight neighbouring elements
+// a lane and the pairs' other halves by shuffles 83.  The token's rotary / 2 angles
+// are computed once, two or so a lane, and pass through shared memory; a lane sits
+// at the same place of each of its rows and keeps the four it needs in registers.
 #pragma once
 
 #include "decode_common.cuh"
@@ -57,6 +57,14 @@ struct NormRopeParams {
 };
 
 constexpr int kNormRopeWarps = 4;
+
+// CTAs an SM: eight where the rows in flight fit the 64 registers a thread that this
+// leaves, else seven (8192 tokens of 40 rows of 128, bf16, not appended: 55 us with eight, 36
+// with seven; D = 256: 23 and 24).
+template <typename T, int D, bool APPEND>
+constexpr int norm_rope_ctas() {
+  return sizeof(T) == 2 && (APPEND || D == 256) ? 8 : 7;
+}
 
 // Four consecutive elements in fp32, in pairs for packed arithmetic.
 struct Wide4 {
@@ -105,7 +113,7 @@ __device__ __forceinline__ float2 turn_pair(float2 x, float c, float s) {
 }
 
 template <typename T, int D, bool APPEND>
-__global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNormRopeWarps * 32, (norm_rope_ctas<T, D, APPEND>())) norm_rope_kernel(const NormRopeParams p) {
   constexpr uint32_t FULL = 0xffffffffu;
   constexpr int LPR = D / 8;                 // lanes per row
   constexpr int RPW = 32 / LPR;              // rows a warp holds at a time
@@ -121,12 +129,12 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const
   pdl_wait();  // a programmatic dependent: nothing of global memory is touched before
 
   // This lane's two chunks: the first and second elements of the pairs 4 ch .. 4 ch + 3
-  // (half-split; behind `rotary` the halves of what is left), or eight neighbours
-  // (interleaved: two pairs in each).
-  const bool rotated = p.interleaved ? ch * 8 < p.rotary : ch * 4 < half;
-  const int rest = ch * 4 - half;
-  const int lo = p.interleaved ? ch * 8 : rotated ? ch * 4 : p.rotary + rest;
-  const int hi = p.interleaved ? lo + 4 : rotated ? lo + half : lo + ((D - p.rotary) >> 1);
+  // (half-split; behind `rotary` the halves of what is left), or (interleaved) two
+  // pairs of each half of the row.  Neighbouring lanes' chunks are neighbours.
+  const int split = p.interleaved ? D : half, rest = ch * 4 - split;
+  const int lo = rest < 0 ? ch * 4 : p.rotary + rest;
+  const int hi = p.interleaved ? lo + D / 2 : rest < 0 ? lo + half : lo + ((D - p.rotary) >> 1);
+  const bool lo_turns = p.interleaved ? lo < p.rotary : rest < 0, hi_turns = p.interleaved ? hi < p.rotary : rest < 0;
 
   // ---- this warp's rows: q heads, then k heads, then (APPEND) v heads -----------------------
   const int64_t slot = APPEND ? p.slots[token] : 0;
@@ -171,11 +179,16 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const
     return static_cast<T*>(is_k ? p.k_cache : p.v_cache) + ((blk * p.hkv + h) * p.block_size + off) * D;
   };
 
-  // This lane's angles: four pairs, or (interleaved) two pairs' in each chunk, both elements' the same.
+  // This lane's angles: four pairs, or (interleaved) two of each chunk.
   Wide4 c = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  if (rotated) {  // half-split: pair 4 ch + e; interleaved: chunk elements (2 e, 2 e + 1) are pair 4 ch + e
-    c = wide4(&cosines[warp][ch * 4]);
-    sn = wide4(&sines[warp][ch * 4]);
+  const int pair0 = p.interleaved ? lo / 2 : lo, pair1 = p.interleaved ? hi / 2 : lo + 2;
+  if (lo_turns) {
+    c.a = *reinterpret_cast<const float2*>(&cosines[warp][pair0]);
+    sn.a = *reinterpret_cast<const float2*>(&sines[warp][pair0]);
+  }
+  if (hi_turns) {
+    c.b = *reinterpret_cast<const float2*>(&cosines[warp][pair1]);
+    sn.b = *reinterpret_cast<const float2*>(&sines[warp][pair1]);
   }
   const Wide4 minus = {make_float2(-sn.a.x, -sn.a.y), make_float2(-sn.b.x, -sn.b.y)};
   const int turned_rows = p.hq + p.hkv;  // of q and k; v rows are copied as they are
@@ -204,15 +217,14 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, 8) norm_rope_kernel(const
           }
         }
         if (turned) {
-          if (rotated) {  // (not rotated: as it is, since 0 times an infinity is not nothing)
-            if (p.interleaved) {
-              x = {turn_pair(x.a, c.a.x, sn.a.x), turn_pair(x.b, c.a.y, sn.a.y)};
-              y = {turn_pair(y.a, c.b.x, sn.b.x), turn_pair(y.b, c.b.y, sn.b.y)};
-            } else {
-              const Wide4 z = turn4(x, c, y, minus);
-              y = turn4(y, c, x, sn);
-              x = z;
-            }
+          // (What does not turn stays as it is: 0 times an infinity is not nothing.)
+          if (p.interleaved) {
+            if (lo_turns) x = {turn_pair(x.a, c.a.x, sn.a.x), turn_pair(x.b, c.a.y, sn.a.y)};
+            if (hi_turns) y = {turn_pair(y.a, c.b.x, sn.b.x), turn_pair(y.b, c.b.y, sn.b.y)};
+          } else if (lo_turns) {
+            const Wide4 z = turn4(x, c, y, minus);
+            y = turn4(y, c, x, sn);
+            x = z;
           }
           a[u].round(x);
           b[u].round(y);
