@@ -379,3 +379,85 @@ def test_a_workspace_shared_with_the_split_decode():
         assert torch.equal(bits(step()), bits(first))
         assert torch.equal(bits(_run(c, workspace=ws)), bits(tree))
     assert torch.count_nonzero(ws[:256 * 1024]).item() == 0
+
+
+@pytest.mark.parametrize("heads", [(4, 1, 64), (4, 2, 128), (2, 1, 256)])
+@pytest.mark.parametrize("window", [0, 37])
+def test_fp32_ranges_shared_by_a_cluster(heads, window):
+    """fp32: the bound on the contexts decides how many CTAs share a range; one to eight here, some without a token."""
+    c = _case([90, 7, 41], 7, heads, F32, seed=33)
+    want = _ref(c, window=window)
+    for most in (90, 100, 200, 400, 800, 100000):
+        ref.assert_near(_run(c, window=window, max_context_len=most), *want, f"{heads} at most {most}")
+    c = _case([1500], 40, heads, F32, seed=34)
+    ref.assert_near(_run(c, window=window), *_ref(c, window=window), f"{heads} long")
+    assert pa.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_in_a_row_without_a_wait(dtype):
+    """Each call's launches may begin while those before still run: forty in a
+    row, of four shapes in turn on one workspace, give what each gives alone."""
+    shapes = [([300, 45, 900], 9, (32, 8, 128)), ([64, 65], 33, (32, 8, 128)), ([2000] * 5, 8, (32, 4, 64)),
+              ([130, 700], 50, (8, 4, 256))]
+    cases = [_case(lens, nodes, heads, dtype, seed=35 + i) for i, (lens, nodes, heads) in enumerate(shapes)]
+    alone = [_run(c) for c in cases]
+    need = max(pa.decode_tree_workspace_size(len(lens), nodes, h[0], h[2], max(lens), h[1]) for lens, nodes, h in shapes)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    outs = [torch.full_like(alone[i % 4], 7.0) for i in range(40)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        _run(cases[i % 4], out=out, workspace=ws, max_context_len=max(shapes[i % 4][0]))
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(bits(out), bits(alone[i % 4])), i
+    assert torch.count_nonzero(ws[:256 * 1024]).item() == 0 and pa.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_two_streams_at_once(dtype):
+    """Calls on two streams, each with its own workspace and output."""
+    cases = [_case([800, 333, 1200], 12, (32, 8, 128), dtype, seed=41), _case([500] * 6, 40, (32, 4, 64), dtype, seed=42)]
+    want = [_run(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [torch.zeros(max(16, pa.decode_tree_workspace_size(6, 64, 32, 128, 1200, 8)), dtype=torch.uint8, device="cuda")
+              for _ in cases]
+    outs = [[torch.empty_like(w) for _ in range(8)] for w in want]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for i, c in enumerate(cases):
+            _run(c, out=outs[i][k], workspace=spaces[i], stream=streams[i], max_context_len=1200)
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        for out in outs[i]:
+            if dtype is F32:  # the bound on the contexts may change how a range is shared, and so the sums' order
+                ref.assert_near(out, *_ref(cases[i]), f"stream {i}")
+            else:
+                assert torch.equal(bits(out), bits(w)), i
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("heads", [(32, 8, 128), (32, 4, 64), (8, 4, 256)])
+def test_a_captured_batch_that_empties(dtype, heads):
+    """One captured call whose batch is padded differently at each replay; rows of sequences without a tree are zero."""
+    lens, nodes = [70, 300, 129, 64, 500], 20
+    c = _case(lens, nodes, heads, dtype, seed=43)
+    tl = torch.full((5,), nodes, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(max(16, pa.decode_tree_workspace_size(5, nodes, heads[0], heads[2], 512, heads[1])), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.full_like(c["q"], 7.0)
+    _run(c, out=out, workspace=ws, tree_lens=tl, max_context_len=512)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _run(c, out=out, workspace=ws, tree_lens=tl, max_context_len=512)
+    for now, trees in (([0, 300, 0, 64, 500], [20, 1, 0, 20, 7]), ([0] * 5, [0] * 5), (lens, [20] * 5), ([1, 0, 0, 0, 0], [1, 0, 0, 0, 0])):
+        c["lens"].copy_(torch.tensor(now, dtype=torch.int32))
+        tl.copy_(torch.tensor(trees, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref.assert_near(out, *_ref(c, tree_lens=tl), f"{now}")
+        for b, n in enumerate(trees):
+            assert torch.count_nonzero(out[b, n if now[b] else 0:]).item() == 0
+    assert pa.device_errors() == 0
