@@ -400,11 +400,10 @@ pa_status_t pa_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   1 <= tree_len <= 64 (PA_ERR_UNSUPPORTED above).  bf16 runs on the tensor
  *   cores, fp32 on CUDA cores.
  *   workspace: for bf16, device memory of at least
- *   pa_decode_tree_workspace_size() bytes, 16-byte aligned, under
- *   pa_decode_splitk's contract: its first PA_COUNTER_BYTES zero before its
- *   first use, and left at zero by every call, so that one workspace serves
- *   this call and pa_decode_splitk's family in any order; calls that share it
- *   must be ordered on one stream; after PA_DEVERR_TIMEOUT zero it again.
+ *   pa_decode_tree_workspace_size() bytes, 16-byte aligned.  Its first
+ *   PA_COUNTER_BYTES, where pa_decode_splitk's family counts, are left as they
+ *   are, so that one workspace serves both in any order; the rest need not be
+ *   initialised.  Calls that share a workspace must be ordered on one stream.
  *   fp32: none (workspace may be NULL).  Two launches for bf16, one for fp32.
  *   Passages: nano-vllm (ovshake) README, "Features" (speculative decoding)
  *   and the speculative-decoding command line (--num-speculative-tokens);

@@ -427,8 +427,7 @@ def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     drafts; bit i of node j's word says that j attends node i (its ancestors and
     itself).  ``tree_lens`` (int32 ``[B]``): nodes of each sequence's tree, when
     they have fewer than T (the rows of the others are zero).  The workspace
-    must be zero-filled before its first use, as ``decode_splitk``'s; it is
-    allocated with torch, its counter region zeroed, if not given.
+    (allocated with torch if not given) may be one that ``decode_splitk`` uses too.
     """
     return (_native_module or _native()).decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, scale,
                                                      softcap, window, max_context_len, tree_lens, out, workspace,

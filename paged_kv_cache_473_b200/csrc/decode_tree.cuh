@@ -22,15 +22,15 @@
 //     twice from DRAM.)
 //
 // Split.  The units, in order, are one line of work: of each, a fixed cost (its Q,
-// masks and rows, counted in tiles) and its tiles.  The line's first
-// part is cut into one range for each CTA (of a row tile or pair); the rest into
-// shorter ranges that CTAs claim when they are done, since SMs stream at rates up
-// to a third apart.  A range is a sequence of pieces of units; loads run on into the
-// next piece while the softmax is still at the last one.  A unit that lies in one
-// range is written as rows of `out`; the pieces of one that is cut are written as
-// partials, at most two per range (the piece that comes from the range before,
-// the one that goes on in the next), and joined by tree_combine_kernel.  Which CTA
-// takes a range changes no bit of the result.
+// masks and rows, counted in tiles) and its tiles.  The line is cut into one range
+// for each CTA (of a row tile or pair).  A range is a sequence of pieces of units;
+// loads run on into the next piece while the softmax is still at the last one.  A
+// unit that lies in one range is written as rows of `out`; the pieces of one that
+// is cut are written as partials, at most two per range (the piece that comes
+// from the range before, the one that goes on in the next), and joined by
+// tree_combine_kernel.  (The line's last 3/16 in shorter ranges, claimed by CTAs that
+// are done: 538 for 495 us on 8 trees of 64 over 16K-128K keys, 124 for 113 on 256 of
+// 24: a claimed range costs its CTA more, some 5 us, than SMs differ.)
 //
 // Warps 0-7: softmax, one row per thread; they also write the rows.  Warp 11: MMA
 // issue, and the load of a piece's Q as soon as the last S of the piece before
@@ -70,12 +70,6 @@ constexpr int kTreeThreads = kTreeWarps * 32;
 // these roles the other way round, 227 so; 7 of 39 nodes 30.5 and 29.3).
 constexpr int kTreeMendWarp = 8, kTreeVWarp = 9, kTreeKWarp = 10, kTreeMmaWarp = 11;
 constexpr int kTreeCombineRows = 8;  // rows of the partials that lie side by side
-constexpr int kTreeMinTiles = 2;    // shortest range: below, a piece's fixed cost outweighs its tiles
-// Claimed ranges: the last 3/16 of the line in up to two per CTA, where a CTA's
-// share is at least kTreeClaimTiles tiles (a shorter share is all one range).
-constexpr int kTreeClaimTiles = 48;
-constexpr int kTreeClaimsPerCta = 2;
-constexpr int kTreeMaxPairs = 4;    // 512 rows in row tiles of one: counters in use
 constexpr int kTreePieces = 4;      // ring of pieces between the roles
 constexpr int kTreeMarks = 2 * kTreePieces;  // pieces whose marks of V are kept: those between the mender and the last epilogue
 
@@ -89,7 +83,7 @@ struct TreeCfg {
   static constexpr int kKVPanelBytes = kTreeTile * 128;
   static constexpr int kKBytes = kPanels * kKVPanelBytes;
   static constexpr int kMaxSmem = 232448;
-  static constexpr int kSharedBytes = D == 256 && QR == 64 ? 3072 : 4096;
+  static constexpr int kSharedBytes = D == 256 && QR == 64 ? 3 * 1024 : 4096;
   static constexpr int kFit = (kMaxSmem - kSharedBytes - kRowTiles * kQBytes) / kKBytes;
   static constexpr int kKStages = (kFit + 1) / 2 < 10 ? (kFit + 1) / 2 : 10;
   static constexpr int kVStages = kFit / 2 < 10 ? kFit / 2 : 10;
@@ -113,7 +107,6 @@ struct TreeCfg {
 struct TreePiece {
   int b, g, t0, t1, tiles;
   int L, n, ulo;  // the sequence's lengths, first attended position
-  int range;
 };
 
 // What the CTA's threads share besides the tiles (behind them, at kBarOff).
@@ -133,40 +126,19 @@ struct TreeShared {
   float m[PAIR ? 1 : 2][PAIR ? 1 : QR];  // running maximum, by tile parity
   float l[PAIR ? 1 : 2][PAIR ? 1 : QR];  // the groups' sums at a piece's end
   long long before[kTreeWarps + 1];      // the line before each warp's part of the batch
-  long long rel0;                        // where the CTA's first range starts: a sequence, and how far in
+  long long rel0;                        // where the CTA's range starts: a sequence, and how far in
   int b0;
   uint32_t tmem;
   int abort;
 };
 
-// The line of work and its ranges: [0, groups) of `per`, then claimed ones of `chunk`.
+// The line of work, in ranges of `per`.
 struct TreeLine {
-  long long total, per, chunk, fixed;  // fixed: that of the first `groups` ranges
-  int groups, ranges;
+  long long total, per;
 
-  __device__ __forceinline__ void cut(long long all, int n) {
-    total = all;
-    groups = n;
-    const long long share = (all + n - 1) / n;
-    if (share < kTreeClaimTiles) {
-      per = max(share, (long long)kTreeMinTiles);
-      chunk = 1;
-      fixed = all;
-      ranges = n;
-    } else {
-      per = share * 13 / 16;
-      fixed = per * n;
-      const long long rest = all - fixed, most = (long long)n * kTreeClaimsPerCta;
-      chunk = max((rest + most - 1) / most, 1ll);
-      ranges = n + (int)((rest + chunk - 1) / chunk);
-    }
-  }
-  __device__ __forceinline__ long long start(int r) const {
-    return min(r < groups ? r * per : fixed + (r - groups) * chunk, r < groups ? fixed : total);
-  }
-  __device__ __forceinline__ int range_of(long long x) const {
-    return x < fixed ? (int)(x / per) : groups + (int)((x - fixed) / chunk);
-  }
+  __device__ __forceinline__ TreeLine(long long all, int n) : total(all), per(max((all + n - 1) / n, 1ll)) {}
+  __device__ __forceinline__ long long start(int r) const { return min(r * per, total); }
+  __device__ __forceinline__ int range_of(long long x) const { return (int)(x / per); }
 };
 
 // Tiles of a unit of this sequence.
@@ -222,20 +194,6 @@ struct TreeWalk {
       load_next(p);
     }
     off = (int)rel;
-  }
-  // The same, to find where that is; before[i]: the line before warp part i of the batch.
-  __device__ __forceinline__ void find(const TreeParams& p, const long long* before, long long from, long long to,
-                                       int lane) {
-    constexpr uint32_t FULL = 0xffffffffu;
-    w = w1 = to;
-    if (from >= to) return;
-    const int part = __popc(__ballot_sync(FULL, lane > 0 && lane < kTreeWarps && before[lane] <= from));
-    long long ahead, all;
-    const long long v = tree_lane_work<COST>(p, part, lane, false, ahead, all);
-    ahead += before[part];
-    const int src = __ffs(__ballot_sync(FULL, v > 0 && from >= ahead && from < ahead + v)) - 1;
-    if (src < 0) return;  // cannot be: from < to <= total
-    start(p, from, to, (part * 32 + src) * tree_scan_step(p), from - __shfl_sync(FULL, ahead, src));
   }
   __device__ __forceinline__ void fit(const TreeParams& p, int len, int nodes) {
     s = tree_fit(p, len, nodes, false);
@@ -360,8 +318,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int i = 1; i <= kTreeWarps; ++i) sh.before[i] += sh.before[i - 1];
   }
   __syncthreads();
-  TreeLine line;
-  line.cut(sh.before[kTreeWarps], gridDim.x / pairs);
+  const TreeLine line(sh.before[kTreeWarps], gridDim.x / pairs);
   before += sh.before[warp];
   const long long from = line.start(grp);
   if (mine > 0 && from >= before && from < before + mine) {
@@ -393,7 +350,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // for a length or a block table.
     TreeWalk<C::kUnitCost> walk;
     TreePiece cur, nxt;
-    int range = grp, u = 0, i = 0, wb = 0, pages = -1, pages2 = -1, first = -1;
+    int u = 0, i = 0, wb = 0, pages = -1, pages2 = -1, first = -1;
     bool more = false, ok = true;
     int4 rec = make_int4(0, 0, 0, 0);  // the unit that starts in this range and goes on: pieces, b, g, nodes
     cur.t1 = 0;
@@ -401,34 +358,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int kt0 = c.ulo & ~(TILE - 1), t = kt0 + c.t0 * TILE + (q << p.log2_box);
       return t < min(c.L, kt0 + c.t1 * TILE) ? p.block_tables[(int64_t)c.b * p.max_blocks + (t >> p.log2_bs)] : -1;
     };
-    auto find = [&]() {  // the next piece of this range, or of the next one claimed
+    auto find = [&]() {  // the next piece
       long long at = 0;
-      while (true) {
-        if (walk.next(p, mt0 * p.q_nodes, nxt, at)) {
-          nxt.range = range;
-          if (nxt.t0 == 0 && nxt.t1 < nxt.tiles)
-            rec = make_int4(line.range_of(at + nxt.tiles - 1) - range + 1, nxt.b, nxt.g, nxt.n);
-          return true;
-        }
-        if (lane < C::kRowTiles && mt0 + lane < p.m_tiles) {  // this range's record, for each row tile
-          const bool has = rec.x > 0 && (mt0 + lane) * p.q_nodes < rec.w;
-          p.ws_rec[(int64_t)range * p.m_tiles + mt0 + lane] = has ? rec : make_int4(0, 0, 0, 0);
-        }
-        rec = make_int4(0, 0, 0, 0);
-        if (line.ranges <= line.groups) return false;
-        int claim = 0;
-        if (lane == 0) claim = atomicAdd(p.queue + pair, 1);
-        range = line.groups + __shfl_sync(FULL, claim, 0);
-        if (range >= line.ranges) return false;
-        walk.find(p, sh.before, line.start(range), line.start(range + 1), lane);
-      }
+      const bool found = walk.next(p, mt0 * p.q_nodes, nxt, at);
+      if (found && nxt.t0 == 0 && nxt.t1 < nxt.tiles)
+        rec = make_int4(line.range_of(at + nxt.tiles - 1) - grp + 1, nxt.b, nxt.g, nxt.n);
+      return found;
     };
     const int boxes = TILE >> p.log2_box, box_rows = 1 << p.log2_box;  // of a tile: 4, 2 or 1
     int issued = 0;
     walk.w = walk.w1 = 0;
-    if (line.start(range) < line.start(range + 1))
-      walk.start(p, line.start(range), line.start(range + 1), sh.b0, sh.rel0);
-    if (blockIdx.x == 0 && lane == 0) p.ws_rec[-1].x = line.ranges;  // how many records there are
+    if (from < line.start(grp + 1)) walk.start(p, from, line.start(grp + 1), sh.b0, sh.rel0);
     while (!*abort_flag) {
       if (i >= cur.t1) {  // the next piece goes into the ring, and the one after it is looked up (at first: both)
         bool stop = false;
@@ -489,6 +429,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (lane == 0) mbar_arrive(bar(sh.rfull[at]));
       issued = n + 1;
       ++i;
+    }
+    if (lane < C::kRowTiles && mt0 + lane < p.m_tiles) {  // the range's record, for each row tile
+      const bool has = rec.x > 0 && (mt0 + lane) * p.q_nodes < rec.w;
+      p.ws_rec[(int64_t)grp * p.m_tiles + mt0 + lane] = has ? rec : make_int4(0, 0, 0, 0);
     }
     if (lane == 0) {  // no more tiles; the ring's place is free, as for a tile
       sh.rows[issued % C::kRing][0] = -2;
@@ -974,7 +918,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int e = 0; e < 4; ++e) marks |= *const_cast<const volatile uint64_t*>(&bad[e]);
       const bool begins = c.t0 == 0, whole = begins && c.t1 == c.tiles;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t slot = ((int64_t)c.range * p.m_tiles + mt) * 2 + (begins ? 1 : 0);
+      const int64_t slot = ((int64_t)grp * p.m_tiles + mt) * 2 + (begins ? 1 : 0);
       float* po = p.ws_o + slot * row_stride * D + r * 4;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
                             ((int64_t)c.b * p.tree_len * p.hq + (int64_t)c.g * G + head) * D;
@@ -1065,10 +1009,9 @@ __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p)
   constexpr int kRows = kTreeCombineRows;
   pdl_wait();  // the partials come from the attention grid
   const int c = blockIdx.x / p.m_tiles, t = blockIdx.x - c * p.m_tiles;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kTreeMaxPairs) p.queue[threadIdx.x] = 0;  // for the next call
-  const int ranges = p.ws_rec[-1].x;
+  const int ranges = gridDim.x / p.m_tiles;
   const int4 rec = p.ws_rec[blockIdx.x];
-  if (c >= ranges || rec.x < 2 || c + rec.x > ranges) return;
+  if (rec.x < 2 || c + rec.x > ranges) return;
   if ((unsigned)rec.y >= (unsigned)p.batch || (unsigned)rec.z >= (unsigned)p.hkv) return;  // left by a call that gave up
   const int G = p.group, row_stride = tree_row_stride(p);
   const int r0 = blockIdx.y * EACH * kRows + (threadIdx.x & (kRows - 1)), col4 = threadIdx.x / kRows;

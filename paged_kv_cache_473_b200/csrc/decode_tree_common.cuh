@@ -29,8 +29,7 @@ struct TreeParams {
   int64_t mask_stride;          // 0: every sequence has the same tree
   float* ws_o;                  // partials (decode_tree.cuh)
   float* ws_ml;
-  int4* ws_rec;                 // one record per (range, row tile); ws_rec[-1].x: how many ranges there are
-  int* queue;                   // ranges claimed, for each CTA of a group (zero between calls)
+  int4* ws_rec;                 // one record per (range, row tile)
   int batch, tree_len, hq, hkv, group;
   int block_size, log2_bs, max_blocks, num_blocks;
   int log2_box;                 // rows of a K/V box: a block's, up to a tile's 64

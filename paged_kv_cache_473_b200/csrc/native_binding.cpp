@@ -269,11 +269,10 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (!ws.defined() && dt == PA_BF16) {
       const size_t need = pa_decode_tree_workspace_size(small(B, c), small(T, c), small(hq, c), small(d, c), most,
                                                         small(kc.size(1), c));
-      if (need > 0) {  // 0: sizes that the call refuses.  The counter region has to start at zero.
+      if (need > 0) {  // 0: sizes that the call refuses
         const c10::cuda::CUDAStreamGuard on(
             c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), c.device.index()));
         ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-        ws.narrow(0, 0, std::min<int64_t>((int64_t)need, PA_COUNTER_BYTES)).zero_();
       }
     } else if (ws.defined() && ws.device() != c.device) {
       c.no("the workspace is on another device");

@@ -117,9 +117,9 @@ cudaError_t launch_tree_simt(TreeParams& p, int head_dim, cudaStream_t st) {
 
 // How the tensor-core kernel takes a call: one CTA per SM, for one row tile of
 // whole nodes or (head_dim 64 and 128, where tensor memory holds two outputs)
-// for two of them.  Workspace: the counter region of the split-K calls, whose
-// first words count the claimed ranges, one record per (range, row tile) behind
-// a header, two partials of `rows` rows for each.
+// for two of them.  Workspace: behind the counter region of the split-K calls, which
+// stays as it is, one record per (range, row tile) and two partials of `rows` rows
+// for each.
 struct TreePlan {
   int q_nodes, m_tiles, grid, rows, records;
   bool pair;
@@ -133,8 +133,8 @@ TreePlan tree_plan(int head_dim, int tree_len, int group) {
   const int share = w.pair ? (w.m_tiles + 1) / 2 : w.m_tiles;  // CTAs that take the same range
   w.grid = std::max(1, sm_count() / share) * share;
   w.rows = (w.q_nodes * group + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows * pa::kTreeCombineRows;
-  w.records = w.grid / share * (1 + pa::kTreeClaimsPerCta) * w.m_tiles;
-  w.rec = pa::kCounterBytes + 256;
+  w.records = w.grid / share * w.m_tiles;
+  w.rec = pa::kCounterBytes;
   w.o = w.rec + align256((size_t)w.records * sizeof(int4));
   w.ml = w.o + align256(2 * (size_t)w.records * w.rows * head_dim * 4);
   w.bytes = w.ml + align256(2 * (size_t)w.records * w.rows * 2 * 4);
@@ -167,30 +167,25 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t s
   if (e != cudaSuccess) return e;
   e = launch_ex(kern, dim3(w.grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  // Records that the call can have (no range is claimed where no share can be
-  // long enough for it), 8 of their rows a block, or 32 where that would be more
-  // than two waves of blocks.  B200: 7 trees of 39 nodes 32.2 us with 8 rows of
-  // every record there might be, 25.8 so; 64 trees of 8 nodes 26.4 with 8 rows, 32.1 with 32.
-  const int groups = w.records / w.m_tiles / (1 + pa::kTreeClaimsPerCta);
-  const long long longest = std::min<long long>(p.max_context, (long long)p.max_blocks * p.block_size);
-  const long long line = (long long)p.batch * p.hkv * (longest / pa::kTreeTile + 2 + Cfg::kUnitCost);
-  const int ranges = line / groups + 1 < pa::kTreeClaimTiles ? groups : groups * (1 + pa::kTreeClaimsPerCta);
+  // 8 rows of a record a block, or 32 where that would be more than two waves of
+  // blocks.  B200: 64 trees of 8 nodes 26.4 us with 8 rows, 32.1 with 32; 7 trees of 39
+  // nodes, with three times the blocks, 32.2 with 8 and 25.8 with 32.
   const int row_blocks = w.rows / pa::kTreeCombineRows;
-  const bool many = 2LL * D * ranges * w.m_tiles * row_blocks > 2 * 2048LL * sm_count();
-  const dim3 grid(ranges * w.m_tiles, many ? (row_blocks + 3) / 4 : row_blocks);
+  const bool many = 2LL * D * w.records * row_blocks > 2 * 2048LL * sm_count();
+  const dim3 grid(w.records, many ? (row_blocks + 3) / 4 : row_blocks);
   return launch_ex(many ? pa::tree_combine_kernel<D, 4> : pa::tree_combine_kernel<D, 1>, grid, dim3(2 * D), 0, st, true, p);
 }
 
 cudaError_t launch_tree(const TreeParams& p, int head_dim, const TreePlan& w, cudaStream_t st) {
-  const bool small = w.rows <= 64;
   switch (head_dim) {
     case 64:
       return w.pair ? launch_tree_t<64, 128, true>(p, w, st) : launch_tree_t<64, 128, false>(p, w, st);
     case 128:
-      if (w.pair) return launch_tree_t<128, 128, true>(p, w, st);
-      return small ? launch_tree_t<128, 64, false>(p, w, st) : launch_tree_t<128, 128, false>(p, w, st);
+      return w.pair ? launch_tree_t<128, 128, true>(p, w, st) : launch_tree_t<128, 128, false>(p, w, st);
     default:
-      return small ? launch_tree_t<256, 64, false>(p, w, st) : launch_tree_t<256, 128, false>(p, w, st);
+      // Up to 64 rows of Q leave room for a third stage of K and of V (256 trees of 24
+      // nodes 124 us, 131 with two; at head_dim 64 and 128 there are enough either way).
+      return w.rows <= 64 ? launch_tree_t<256, 64, false>(p, w, st) : launch_tree_t<256, 128, false>(p, w, st);
   }
 }
 
@@ -347,7 +342,6 @@ pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cac
     return PA_OK;
   }
   char* ws = static_cast<char*>(workspace);
-  p.queue = reinterpret_cast<int*>(ws);
   p.ws_rec = reinterpret_cast<int4*>(ws + w.rec);
   p.ws_o = reinterpret_cast<float*>(ws + w.o);
   p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
