@@ -96,7 +96,10 @@ struct TreeCfg {
   // Tiles that S runs ahead of P V (three with two stages of V: 61.4 for 58.7 us on
   // 121 trees of 44 nodes, head_dim 256).
   static constexpr int kLag = PAIR || kVStages < 3 ? 2 : 3;
-  static constexpr int kUnitCost = D <= 64 ? 4 : D <= 128 ? 2 : 1;  // of a unit, in tiles of this head_dim (about 1.5 us)
+  // What a unit costs besides its tiles, in tiles: its Q, masks, last tile's latency and
+  // rows.  None counted, 64 trees of 8 nodes at head_dim 64 take 34 us for 26; 2 and 1
+  // instead of 4 and 3, 128 of 16 at 128 233 for 218, 256 of 24 at 256 114 for 106.
+  static constexpr int kUnitCost = D == 64 ? 4 : PAIR ? 2 : D == 128 ? 4 : 3;
   static constexpr int kOCol = 0;                       // O (PAIR: a second one D columns on)
   static constexpr int kSCol = 256;                     // four S buffers, two per group
   static_assert(!PAIR || D <= 128, "tensor memory");
