@@ -1006,10 +1006,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 //   out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p,
 // in piece order.  blockIdx.y: 8 EACH rows; a thread has four columns of EACH of
 // them, and neighbouring threads neighbouring rows, as the partials lie.  M runs
-// along, so that no load waits for another.
+// along, and DEPTH pieces are loaded at a time (two of 74 on one unit: 62 us, four
+// 56, eight 55; but eight cost registers: 256 trees of 24 nodes 108 for 106).
 template <int D, int EACH>
 __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p) {
-  constexpr int kRows = kTreeCombineRows;
+  constexpr int kRows = kTreeCombineRows, DEPTH = EACH == 1 ? 4 : 2;
   pdl_wait();  // the partials come from the attention grid
   const int c = blockIdx.x / p.m_tiles, t = blockIdx.x - c * p.m_tiles;
   const int ranges = gridDim.x / p.m_tiles;
@@ -1029,11 +1030,11 @@ __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p)
     den[j] = 0.f;
     acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  for (int k0 = 0; k0 < rec.x; k0 += 2) {
-    float2 ml[2][EACH];
-    float4 o[2][EACH];
+  for (int k0 = 0; k0 < rec.x; k0 += DEPTH) {
+    float2 ml[DEPTH][EACH];
+    float4 o[DEPTH][EACH];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < DEPTH; ++k)
 #pragma unroll
       for (int j = 0; j < EACH; ++j) {
         const int r = r0 + j * kRows;
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(2 * D) tree_combine_kernel(const TreeParams p)
         }
       }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < DEPTH; ++k)
 #pragma unroll
       for (int j = 0; j < EACH; ++j) {
         const float top = fmaxf(M[j], ml[k][j].x), ref = top == -CUDART_INF_F ? 0.f : top;

@@ -167,11 +167,14 @@ cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t s
   if (e != cudaSuccess) return e;
   e = launch_ex(kern, dim3(w.grid), dim3(pa::kTreeThreads), Cfg::kSmemBytes, st, true, qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  // 8 rows of a record a block, or 32 where that would be more than two waves of
-  // blocks.  B200: 64 trees of 8 nodes 26.4 us with 8 rows, 32.1 with 32; 7 trees of 39
-  // nodes, with three times the blocks, 32.2 with 8 and 25.8 with 32.
+  // 8 rows of a record a block, or 32 where the records that can be in use (one for
+  // each unit at most) would make more than two waves of blocks so.  B200: 64 trees of
+  // 8 nodes 26.4 us with 8 rows, 32.1 with 32; 7 trees of 39 nodes, with three times
+  // the blocks, 32.2 with 8 and 25.8 with 32; one tree of 39 nodes on 22K keys (8 units of
+  // 19 pieces) 42 with 8, 51 with 32.
+  const long long cut = std::min<long long>(w.records, (long long)p.batch * p.hkv * w.m_tiles);
   const int row_blocks = w.rows / pa::kTreeCombineRows;
-  const bool many = 2LL * D * w.records * row_blocks > 2 * 2048LL * sm_count();
+  const bool many = 2LL * D * cut * row_blocks > 2 * 2048LL * sm_count();
   const dim3 grid(w.records, many ? (row_blocks + 3) / 4 : row_blocks);
   return launch_ex(many ? pa::tree_combine_kernel<D, 4> : pa::tree_combine_kernel<D, 1>, grid, dim3(2 * D), 0, st, true, p);
 }
