@@ -461,3 +461,20 @@ def test_a_captured_batch_that_empties(dtype, heads):
         for b, n in enumerate(trees):
             assert torch.count_nonzero(out[b, n if now[b] else 0:]).item() == 0
     assert pa.device_errors() == 0
+
+
+@pytest.mark.parametrize("heads,nodes", [((32, 8, 128), 9), ((32, 8, 128), 40), ((8, 4, 256), 60), ((32, 4, 64), 8)])
+def test_what_a_workspace_holds_before_does_not_matter(heads, nodes):
+    """Any bytes in it give the same result, and the split decode's counters are left as they are."""
+    lens = [90, 1700, 400]
+    c = _case(lens, nodes, heads, seed=44)
+    want = _run(c)
+    ref.assert_near(want, *_ref(c), f"{heads}")
+    need = pa.decode_tree_workspace_size(3, nodes, heads[0], heads[2], 1700, heads[1])
+    for fill in (0xA5, 0x7F, 0xFF):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        assert torch.equal(bits(_run(c, workspace=ws)), bits(want))
+        assert torch.equal(ws[:256 * 1024], torch.full((256 * 1024,), fill, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(pa.PagedAttnError):
+        _run(c, workspace=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))
+    assert pa.device_errors() == 0
