@@ -49,6 +49,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // the aligned forms take a warp as a whole
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // What lies at `p` of this CTA's shared memory in that of the cluster's CTA `rank`.
