@@ -94,8 +94,9 @@ pa_status_t pa_bm_append_slots(pa_block_manager* bm, const int64_t* seq_ids, con
  * and token_ids [num_token_ids] (may be NULL with 0) are the ids of the last
  * num_token_ids kept positions, which were appended without.  When every
  * position before them is known, the blocks they fill are added to the prefix
- * cache and later appends with ids go on where these end; else they are not
- * used.  PA_ERR_INVALID when more ids are given than kept positions were
+ * cache (those that no other sequence holds: a fork made before the cut may
+ * still write there) and later appends with ids go on where these end; else they
+ * are not used.  PA_ERR_INVALID when more ids are given than kept positions were
  * appended without.  A block that the cut leaves partly filled is taken out of
  * the prefix cache; cutting inside an earlier block whose ids were known makes
  * the ids of that block unknown.

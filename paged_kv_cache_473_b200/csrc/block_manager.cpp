@@ -125,8 +125,12 @@ struct pa_block_manager {
   }
 
   // The next unknown position of a sequence holds this token: a block that is
-  // filled with known tokens is registered in the prefix cache.  Out of host
-  // memory, the ids of that block (and so of what follows) stay unknown.
+  // filled with known tokens is registered in the prefix cache, if this sequence
+  // alone holds it.  (Another holder, forked while the ids were unknown, may cut
+  // into the block or move its rows and then, once alone, write to it in place:
+  // every holder of a registered block knows all of its ids, until it cuts into
+  // the block, which unregisters it.)  Out of host memory, the ids of that block
+  // (and so of what follows) stay unknown.
   void learn(Seq& s, int64_t token) {
     try {
       s.tail_tokens.push_back(token);
@@ -134,7 +138,8 @@ struct pa_block_manager {
       if (s.known % block_size != 0) return;
       const uint64_t parent = s.last_full_hash(), h = block_hash(parent, s.tail_tokens.data(), block_size);
       s.hashes.push_back(h);
-      register_full(s.blocks[s.known / block_size - 1], parent, s.tail_tokens.data(), h);
+      const int32_t id = s.blocks[s.known / block_size - 1];
+      if (blocks[id].ref == 1) register_full(id, parent, s.tail_tokens.data(), h);
       s.tail_tokens.clear();
     } catch (...) {
       s.tail_tokens.clear();
