@@ -403,7 +403,11 @@ pa_status_t pa_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   pa_decode_tree_workspace_size() bytes, 16-byte aligned.  Its first
  *   PA_COUNTER_BYTES, where pa_decode_splitk's family counts, are left as they
  *   are, so that one workspace serves both in any order; the rest need not be
- *   initialised.  Calls that share a workspace must be ordered on one stream.
+ *   initialised.  The size is that of the current device and does not fall as
+ *   tree_len, num_q_heads / num_kv_heads or head_dim grow (batch and
+ *   max_context_len do not matter), so that a workspace sized for the largest
+ *   of each serves every call below.  Calls that share a workspace must be
+ *   ordered on one stream.
  *   fp32: none (workspace may be NULL).  Two launches for bf16, one for fp32.
  *   Passages: nano-vllm (ovshake) README, "Features" (speculative decoding)
  *   and the speculative-decoding command line (--num-speculative-tokens);

@@ -141,6 +141,19 @@ TreePlan tree_plan(int head_dim, int tree_len, int group) {
   return w;
 }
 
+// What a workspace for trees of tree_len nodes holds: what such a call needs, and every
+// call with fewer nodes, heads per kv head or dims does, some of which have more
+// records (32 nodes of 8 heads are two row tiles on every SM; 48 are three, and two
+// CTAs share a range).  A call has at most one record an SM, or two with pairs of row tiles.
+size_t tree_workspace_bytes(int head_dim, int tree_len, int group) {
+  const size_t rows = (size_t)std::min(tree_len * group, pa::kTreeRows), sms = std::max(1, sm_count());
+  const size_t padded = (rows + pa::kTreeCombineRows - 1) / pa::kTreeCombineRows * pa::kTreeCombineRows;
+  const size_t records = tree_len * group > pa::kTreeRows ? 2 * sms : sms;
+  const size_t columns = std::max(records * std::min(head_dim, 128), sms * head_dim);  // no pairs at head_dim 256
+  return pa::kCounterBytes + align256(records * sizeof(int4)) + align256(2 * columns * padded * 4) +
+         align256(2 * records * padded * 2 * 4);
+}
+
 // q as a 3-D tensor [batch * tree_len][num_q_heads][head_dim]; a box is 64
 // columns (128 B) x one kv head's heads x the nodes of a row tile.
 bool encode_q_map(CUtensorMap* map, const TreeParams& p, int head_dim) {
@@ -286,7 +299,7 @@ size_t pa_decode_tree_workspace_size(int32_t batch, int32_t tree_len, int32_t nu
   if (batch <= 0 || tree_len <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_kv_heads <= 0) return 0;
   if (tree_len > pa::kMaxTreeNodes || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup)
     return 0;
-  return tree_plan(head_dim, tree_len, num_q_heads / num_kv_heads).bytes;
+  return tree_workspace_bytes(head_dim, tree_len, num_q_heads / num_kv_heads);
 }
 
 pa_status_t pa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
