@@ -433,8 +433,8 @@ size_t pa_decode_tree_workspace_size(int32_t batch, int32_t tree_len, int32_t nu
  *   position base + accepted[b][i], becomes position base + i, i < a, with
  *   base = context_lens[b] - n and n as in pa_decode_tree; the rows of the
  *   other nodes are left as they are.  new_lens[b] = base + a (may be NULL;
- *   must not be context_lens, which other CTAs still read).  The copies are
- *   bit-exact.
+ *   must not overlap the lengths, paths or tables that the call reads, which
+ *   other CTAs still look at: PA_ERR_INVALID).  The copies are bit-exact.
  *   k_cache, v_cache: [num_layers][num_blocks][num_kv_heads][block_size]
  *   [head_dim], one block table for all layers; num_layers = 1 for the cache
  *   of one layer.

@@ -445,7 +445,7 @@ def commit_tree(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torc
     ``accepted``: int32 ``[B, A]``, the path's node numbers in order (strictly
     increasing), the first ``accept_lens[b]`` of a row; ``tree_len`` /
     ``tree_lens``: nodes of the trees, as in ``decode_tree``.  Returns the new
-    context lengths (``new_lens``, int32 ``[B]``; not ``context_lens`` itself).
+    context lengths (``new_lens``, int32 ``[B]``; no memory of the call's inputs).
     """
     return (_native_module or _native()).commit_tree(k_cache, v_cache, block_tables, context_lens, accepted,
                                                      accept_lens, tree_len, tree_lens, new_lens, stream)

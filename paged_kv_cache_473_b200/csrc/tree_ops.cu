@@ -85,6 +85,13 @@ pa_status_t check_norm_rope(const NormRopeParams& p, int32_t num_tokens, int32_t
   return PA_OK;
 }
 
+// ---- commit ---------------------------------------------------------------------------
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // ---- tree attention -------------------------------------------------------------------
 
 template <int D>
@@ -388,7 +395,14 @@ pa_status_t pa_commit_tree(void* k_cache, void* v_cache, int32_t num_layers, con
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
       !aligned(tree_lens, 4) || !aligned(accepted, 4) || !aligned(accept_lens, 4) || !aligned(new_lens, 4))
     return PA_ERR_INVALID;
-  if (new_lens == context_lens) return PA_ERR_INVALID;
+  // One CTA of a sequence writes its new length while the others may still read these.
+  const size_t lens_bytes = 4 * (size_t)batch;
+  if (new_lens && (overlap(new_lens, lens_bytes, context_lens, lens_bytes) ||
+                   overlap(new_lens, lens_bytes, accept_lens, lens_bytes) ||
+                   (tree_lens && overlap(new_lens, lens_bytes, tree_lens, lens_bytes)) ||
+                   overlap(new_lens, lens_bytes, accepted, lens_bytes * max_accept) ||
+                   overlap(new_lens, lens_bytes, block_tables, lens_bytes * max_blocks_per_seq)))
+    return PA_ERR_INVALID;
   const long long blocks = (2LL * num_layers * token_chunks + pa::kCommitThreads - 1) / pa::kCommitThreads;
   if (blocks > INT_MAX) return PA_ERR_UNSUPPORTED;
 
