@@ -40,11 +40,11 @@ class PagedAttnError(RuntimeError):
 
 def _load_library() -> ctypes.CDLL:
     path = _build.LIB
-    if not _build.up_to_date():
+    if not _build.library_up_to_date():
         try:
-            path = _build.build()
+            path = _build.build_library()
         except Exception as e:  # noqa: BLE001
-            if not (os.path.exists(path) and os.path.exists(_build.NATIVE)):
+            if not os.path.exists(path):
                 raise ImportError(f"libpagedattn.so is missing and could not be built: {e}") from e
     lib = ctypes.CDLL(path)
     lib.pa_write_kv.argtypes = [_c_vp, _c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
@@ -376,6 +376,11 @@ def _native():
     global _native_module
     if _native_module is None:
         _lib()
+        try:
+            _build.build_native()
+        except Exception as e:  # noqa: BLE001
+            if not os.path.exists(_build.NATIVE):
+                raise ImportError(f"the native module of the drafting step's calls is missing and could not be built: {e}") from e
         from . import _native as module
 
         module.set_error_class(PagedAttnError)

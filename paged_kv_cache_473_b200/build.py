@@ -44,16 +44,26 @@ def _nvcc() -> str:
     return cand
 
 
+def _headers() -> list:
+    return sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
 def sources() -> list:
+    """What the library is made of."""
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(ROOT, "include", "*.h")))
+                  [u for u in UNITS if u.endswith(".cpp")]) + _headers()
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(NATIVE)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
-    return all(os.path.getmtime(s) <= t for s in sources())
+def _newer(target: str, than: list) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(s) <= os.path.getmtime(target) for s in than)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, sources())
+
+
+def native_up_to_date() -> bool:
+    return _newer(NATIVE, [NATIVE_SRC, *_headers()])
 
 
 def _object(unit: str) -> str:
@@ -70,6 +80,12 @@ def _fresh(obj: str) -> bool:
     return all(os.path.exists(d) and os.path.getmtime(d) <= t for d in deps)
 
 
+def _run(cmd: list, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+
+
 def _compile(unit: str, force: bool, verbose: bool, extra_flags) -> str:
     obj = _object(unit)
     if not force and _fresh(obj):
@@ -77,9 +93,7 @@ def _compile(unit: str, force: bool, verbose: bool, extra_flags) -> str:
     tmp = f"{obj}.tmp{os.getpid()}"
     cmd = [_nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-MMD", "-MF", tmp + ".d",
            "-c", "-o", tmp, unit]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    _run(cmd, verbose)
     os.replace(tmp + ".d", obj + ".d")
     os.replace(tmp, obj)
     return obj
@@ -90,7 +104,7 @@ def _torch_flags() -> tuple:
     import torch
     from torch.utils import cpp_extension
 
-    inc = [sysconfig.get_paths()["include"], "/usr/local/cuda/include", *cpp_extension.include_paths()]
+    inc = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(device_type="cuda")]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
     return ([abi, *[x for d in inc for x in ("-isystem", d)]],
@@ -104,35 +118,52 @@ def _compile_native(force: bool, verbose: bool) -> str:
     tmp = f"{obj}.tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *_torch_flags()[0], "-MMD", "-MF", tmp + ".d", "-MT", "object", "-c",
            "-o", tmp, NATIVE_SRC]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    _run(cmd, verbose)
     os.replace(tmp + ".d", obj + ".d")
     os.replace(tmp, obj)
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    if not force and up_to_date():
+def build_library(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """The library alone: nvcc is all it needs."""
+    if not force and library_up_to_date():
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
-    with ThreadPoolExecutor(len(UNITS) + 1) as pool:
-        native = pool.submit(_compile_native, force, verbose)
+    with ThreadPoolExecutor(len(UNITS)) as pool:
         objs = list(pool.map(lambda u: _compile(u, force, verbose, extra_flags), UNITS))
-        native = native.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    _run([_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def _link_native(obj: str, verbose: bool) -> str:
     tmp = NATIVE + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, native, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
-           *_torch_flags()[1]]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+          *_torch_flags()[1]], verbose)
     os.replace(tmp, NATIVE)
+    return NATIVE
+
+
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """The Python entry of the per-step calls, which needs g++, the headers of
+    torch and Python, and LIB, to which it is linked."""
+    if not force and native_up_to_date():
+        return NATIVE
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    return _link_native(_compile_native(force, verbose), verbose)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
+    """Both, compiled at the same time.  Where the native module cannot be built
+    this raises, with the library in place."""
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with ThreadPoolExecutor(1) as pool:
+        stale = force or not native_up_to_date()
+        obj = pool.submit(_compile_native, force, verbose) if stale else None
+        build_library(force, verbose, extra_flags)
+        if obj is not None:
+            _link_native(obj.result(), verbose)
     return LIB
 
 
