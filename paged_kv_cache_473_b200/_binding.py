@@ -379,8 +379,9 @@ def _native():
         try:
             _build.build_native()
         except Exception as e:  # noqa: BLE001
-            if not os.path.exists(_build.NATIVE):
-                raise ImportError(f"the native module of the drafting step's calls is missing and could not be built: {e}") from e
+            if not (os.path.exists(_build.NATIVE) and _build.native_fits_torch()):
+                raise ImportError("the native module of the drafting step's calls is missing, or was built for "
+                                  f"another torch, and could not be built: {e}") from e
         from . import _native as module
 
         module.set_error_class(PagedAttnError)

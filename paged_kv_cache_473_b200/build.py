@@ -1,10 +1,12 @@
 """Build the sm_100a shared library ``libpagedattn.so`` in-tree with nvcc.
 
 Each translation unit is compiled to an object of its own, the units at the
-same time, and only those whose sources changed; then they are linked."""
+same time, and only those whose sources or flags changed; then they are linked.
+What a file was made with stands in a stamp beside its object."""
 
 from __future__ import annotations
 
+import contextlib
 import glob
 import os
 import shutil
@@ -12,6 +14,7 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -35,6 +38,7 @@ NVCC_FLAGS = [
     "-Xcompiler",
     "-fPIC",
 ]
+NATIVE_FLAGS = ["-O2", "-std=c++17", "-fPIC"]
 
 
 def _nvcc() -> str:
@@ -63,16 +67,54 @@ def library_up_to_date() -> bool:
 
 
 def native_up_to_date() -> bool:
-    return _newer(NATIVE, [NATIVE_SRC, *_headers()])
+    return _newer(NATIVE, [NATIVE_SRC, *_headers()]) and native_fits_torch()
+
+
+def native_fits_torch() -> bool:
+    """Whether the native module there is was built for the torch that is installed."""
+    return _made_with(NATIVE) in (None, _native_key())
+
+
+def _stamp(target: str) -> str:
+    return os.path.join(OBJ_DIR, os.path.basename(target) + ".made")
+
+
+def _made_with(target: str) -> Optional[str]:
+    """What a file was made with; None where that is not known (it came without its objects)."""
+    try:
+        with open(_stamp(target)) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
+def _made(tmp: str, target: str, key: str) -> None:
+    """A file is complete: it takes its place, with its stamp (none at all in between)."""
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(_stamp(target))
+    os.replace(tmp, target)
+    with open(tmp + ".made", "w") as f:
+        f.write(key)
+    os.replace(tmp + ".made", _stamp(target))
+
+
+def _library_key(extra_flags) -> str:
+    return " ".join([*NVCC_FLAGS, *(extra_flags or [])])
+
+
+def _native_key() -> str:
+    import torch
+
+    return " ".join([*NATIVE_FLAGS, "torch", torch.__version__, str(torch.compiled_with_cxx11_abi())])
 
 
 def _object(unit: str) -> str:
     return os.path.join(OBJ_DIR, os.path.basename(unit) + ".o")
 
 
-def _fresh(obj: str) -> bool:
-    """Whether an object is newer than every source its compiler read."""
-    if not (os.path.exists(obj) and os.path.exists(obj + ".d")):
+def _fresh(obj: str, key: str) -> bool:
+    """Whether an object was made with these flags and is newer than every source its compiler read."""
+    if not (os.path.exists(obj) and os.path.exists(obj + ".d")) or _made_with(obj) != key:
         return False
     with open(obj + ".d") as f:
         deps = f.read().replace("\\\n", " ").split(":", 1)[1].split()
@@ -87,15 +129,15 @@ def _run(cmd: list, verbose: bool) -> None:
 
 
 def _compile(unit: str, force: bool, verbose: bool, extra_flags) -> str:
-    obj = _object(unit)
-    if not force and _fresh(obj):
+    obj, key = _object(unit), _library_key(extra_flags)
+    if not force and _fresh(obj, key):
         return obj
     tmp = f"{obj}.tmp{os.getpid()}"
     cmd = [_nvcc(), *NVCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), "-MMD", "-MF", tmp + ".d",
            "-c", "-o", tmp, unit]
     _run(cmd, verbose)
     os.replace(tmp + ".d", obj + ".d")
-    os.replace(tmp, obj)
+    _made(tmp, obj, key)
     return obj
 
 
@@ -112,28 +154,30 @@ def _torch_flags() -> tuple:
 
 
 def _compile_native(force: bool, verbose: bool) -> str:
-    obj = _object(NATIVE_SRC)
-    if not force and _fresh(obj):
+    obj, key = _object(NATIVE_SRC), _native_key()
+    if not force and _fresh(obj, key):
         return obj
     tmp = f"{obj}.tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *_torch_flags()[0], "-MMD", "-MF", tmp + ".d", "-MT", "object", "-c",
+    cmd = ["g++", *NATIVE_FLAGS, *_torch_flags()[0], "-MMD", "-MF", tmp + ".d", "-MT", "object", "-c",
            "-o", tmp, NATIVE_SRC]
     _run(cmd, verbose)
     os.replace(tmp + ".d", obj + ".d")
-    os.replace(tmp, obj)
+    _made(tmp, obj, key)
     return obj
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """The library alone: nvcc is all it needs."""
-    if not force and library_up_to_date():
+    """The library alone: nvcc is all it needs.  One that was made with other flags is made
+    again (what opens the library takes it as it is, an instrumented one too)."""
+    key = _library_key(extra_flags)
+    if not force and library_up_to_date() and _made_with(LIB) in (None, key):
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     with ThreadPoolExecutor(len(UNITS)) as pool:
         objs = list(pool.map(lambda u: _compile(u, force, verbose, extra_flags), UNITS))
     tmp = LIB + f".tmp{os.getpid()}"
     _run([_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs], verbose)
-    os.replace(tmp, LIB)
+    _made(tmp, LIB, key)
     return LIB
 
 
@@ -141,7 +185,7 @@ def _link_native(obj: str, verbose: bool) -> str:
     tmp = NATIVE + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
           *_torch_flags()[1]], verbose)
-    os.replace(tmp, NATIVE)
+    _made(tmp, NATIVE, _native_key())
     return NATIVE
 
 

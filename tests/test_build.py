@@ -103,3 +103,45 @@ def test_only_what_changed_is_built(tree):
     os.utime(os.path.join(bld.OBJ_DIR, "tree_ops.cu.o"), (1, 1))
     bld.build()
     assert c.compiled() == ["tree_ops.cu"]
+
+
+def test_objects_of_other_flags_are_not_reused(tree):
+    c = tree()
+    bld.build(force=True, extra_flags=["-DINSTRUMENTED"])
+    c.compiled()
+    assert bnd._build.library_up_to_date()  # as it is, for what opens it
+    bld.build()
+    assert c.compiled() == LIBRARY
+    bld.build()
+    assert c.compiled() == []
+    bld.build(extra_flags=["-DINSTRUMENTED"])
+    assert c.compiled() == LIBRARY
+    os.utime(bld.LIB, (1, 1))
+    bld.build()  # a source changed since: all units anew, not only the stale one
+    assert c.compiled() == LIBRARY
+
+
+def test_another_torch_makes_the_native_module_anew(tree, monkeypatch):
+    import torch
+
+    c = tree()
+    bld.build()
+    c.compiled()
+    monkeypatch.setattr(torch, "__version__", "99.1")
+    bld.build()
+    assert c.compiled() == ["native_binding.cpp"]
+    tree("g++")
+    monkeypatch.setattr(torch, "__version__", "99.2")
+    monkeypatch.setattr(bnd, "_native_module", None)
+    with pytest.raises(ImportError, match="another torch"):
+        bnd.qk_norm_rope(None, None, None, None)
+
+
+def test_what_came_without_its_objects_is_taken_by_its_time(tree):
+    c = tree()
+    bld.build()
+    for stamp in (bld._stamp(bld.LIB), bld._stamp(bld.NATIVE)):
+        os.remove(stamp)
+    c.compiled()
+    bld.build()
+    assert c.compiled() == []
