@@ -107,6 +107,18 @@ struct Call {
     if (!p && PyErr_Occurred()) throw PyRaised();
     return static_cast<pa_stream_t>(p);
   }
+  // A new tensor that the call uses on `on`: from that stream's memory, which work queued on
+  // another stream no longer uses.  One that the caller gets is not given to others while
+  // the current stream, where it may be used next, still does.
+  at::Tensor make(c10::IntArrayRef shape, const at::TensorOptions& options, pa_stream_t on, bool returned = true) const {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device.index());
+    if (current.stream() == reinterpret_cast<cudaStream_t>(on)) return at::empty(shape, options);
+    const c10::cuda::CUDAStreamGuard guard(
+        c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(on), device.index()));
+    const at::Tensor t = at::empty(shape, options);
+    if (returned) t.record_stream(current);
+    return t;
+  }
   void check(pa_status_t st, const char* function) const {
     if (st == PA_OK) return;
     PyObject* e = PyObject_CallFunction(g_error_class, "is", (int)st, function);
@@ -168,8 +180,6 @@ struct Rotation {
   }
 };
 
-at::Tensor like(const at::Tensor& t, c10::IntArrayRef shape) { return at::empty(shape, t.options()); }
-
 // q, k, positions, inv_freq, rotary_dim, q_weight, k_weight, eps, interleaved, q_out, k_out, stream -> (q_out, k_out)
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded(n_args, 12, [&]() -> PyObject* {
@@ -180,8 +190,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const pa_dtype_t dt = dtype_code(q);
     const c10::cuda::CUDAGuard guard(c.device);
     at::Tensor q_out = tensor(a[9], "q_out", true), k_out = tensor(a[10], "k_out", true);
-    if (!q_out.defined()) q_out = like(q, {r.n, r.hq, r.d});
-    if (!k_out.defined()) k_out = like(q, {r.n, r.hkv, r.d});
+    const pa_stream_t stream = c.stream(a[11]);
+    if (!q_out.defined()) q_out = c.make({r.n, r.hq, r.d}, q.options(), stream);
+    if (!k_out.defined()) k_out = c.make({r.n, r.hkv, r.d}, q.options(), stream);
     c.is(q_out, q.scalar_type(), "q_out");
     c.is(k_out, q.scalar_type(), "k_out");
     c.check(pa_qk_norm_rope(q.data_ptr(), c.rows(q, r.n, r.hq, r.d, "q"), k.data_ptr(), c.rows(k, r.n, r.hkv, r.d, "k"),
@@ -190,7 +201,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                             static_cast<const float*>(c.ptr(r.inv_freq, "inv_freq")), r.rotary, truth(a[8]),
                             static_cast<const int32_t*>(c.ptr(r.positions, "positions")), small(r.n, c), small(r.hq, c),
                             small(r.hkv, c), small(r.d, c), q_out.data_ptr(), c.rows(q_out, r.n, r.hq, r.d, "q_out"),
-                            k_out.data_ptr(), c.rows(k_out, r.n, r.hkv, r.d, "k_out"), dt, c.stream(a[11])),
+                            k_out.data_ptr(), c.rows(k_out, r.n, r.hkv, r.d, "k_out"), dt, stream),
             "pa_qk_norm_rope");
     PyObject* out = PyTuple_New(2);
     if (!out) throw PyRaised();
@@ -215,7 +226,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (slots.numel() != r.n) c.no("one slot per token is needed");
     const c10::cuda::CUDAGuard guard(c.device);
     at::Tensor q_out = tensor(a[13], "q_out", true);
-    if (!q_out.defined()) q_out = like(q, {r.n, r.hq, r.d});
+    const pa_stream_t stream = c.stream(a[14]);
+    if (!q_out.defined()) q_out = c.make({r.n, r.hq, r.d}, q.options(), stream);
     else if (q_out.sizes() != q.sizes()) c.no("q_out has q's shape");
     c.is(v, q.scalar_type(), "v");
     c.is(kc, q.scalar_type(), "k_cache");
@@ -230,7 +242,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                            static_cast<const int32_t*>(c.ptr(r.positions, "positions")),
                            static_cast<const int64_t*>(c.ptr(slots, "slot_mapping")), small(r.n, c), small(r.hq, c),
                            small(r.hkv, c), small(r.d, c), c.ptr(q_out, "q_out"), c.ptr(kc, "k_cache"),
-                           c.ptr(vc, "v_cache"), small(kc.size(0), c), small(kc.size(2), c), dt, c.stream(a[14])),
+                           c.ptr(vc, "v_cache"), small(kc.size(0), c), small(kc.size(2), c), dt, stream),
             "pa_rope_append");
     return a[13] != Py_None ? Py_NewRef(a[13]) : THPVariable_Wrap(q_out);
   });
@@ -255,7 +267,8 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (tree_lens.defined() && tree_lens.numel() != B) c.no("one tree length per sequence is needed");
     const c10::cuda::CUDAGuard guard(c.device);
     at::Tensor out = tensor(a[11], "out", true), ws = tensor(a[12], "workspace", true);
-    if (!out.defined()) out = like(q, q.sizes());
+    const pa_stream_t stream = c.stream(a[13]);
+    if (!out.defined()) out = c.make(q.sizes(), q.options(), stream);
     else if (out.sizes() != q.sizes()) c.no("out has q's shape");
     c.is(kc, q.scalar_type(), "k_cache");
     c.is(vc, q.scalar_type(), "v_cache");
@@ -265,15 +278,10 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     c.is(tree_lens, at::kInt, "tree_lens");
     c.is(mask, at::kLong, "tree_mask");
     const int32_t most = integer32(a[9], "max_context_len");
-    const pa_stream_t stream = c.stream(a[13]);
     if (!ws.defined() && dt == PA_BF16) {
       const size_t need = pa_decode_tree_workspace_size(small(B, c), small(T, c), small(hq, c), small(d, c), most,
                                                         small(kc.size(1), c));
-      if (need > 0) {  // 0: sizes that the call refuses
-        const c10::cuda::CUDAStreamGuard on(
-            c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), c.device.index()));
-        ws = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
-      }
+      if (need > 0) ws = c.make({(int64_t)need}, q.options().dtype(at::kByte), stream, false);  // 0: sizes that the call refuses
     } else if (ws.defined() && ws.device() != c.device) {
       c.no("the workspace is on another device");
     }
@@ -307,7 +315,8 @@ PyObject* commit_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (take.numel() != B || (tree_lens.defined() && tree_lens.numel() != B)) c.no("one length per sequence is needed");
     const c10::cuda::CUDAGuard guard(c.device);
     at::Tensor new_lens = tensor(a[8], "new_lens", true);
-    if (!new_lens.defined()) new_lens = at::empty({B}, kc.options().dtype(at::kInt));
+    const pa_stream_t stream = c.stream(a[9]);
+    if (!new_lens.defined()) new_lens = c.make({B}, kc.options().dtype(at::kInt), stream);
     else if (new_lens.numel() != B) c.no("one new length per sequence is needed");
     c.is(vc, kc.scalar_type(), "v_cache");
     c.is(tables, at::kInt, "block_tables");
@@ -322,7 +331,7 @@ PyObject* commit_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                            integer32(a[6], "tree_len"), i32(path, "accepted"), small(path.size(1), c),
                            i32(take, "accept_lens"), small(B, c), small(kc.size(o + 1), c), small(kc.size(o + 3), c),
                            small(kc.size(o + 2), c), small(tables.size(1), c), small(kc.size(o), c),
-                           i32(new_lens, "new_lens"), dt, c.stream(a[9])),
+                           i32(new_lens, "new_lens"), dt, stream),
             "pa_commit_tree");
     return a[8] != Py_None ? Py_NewRef(a[8]) : THPVariable_Wrap(new_lens);
   });

@@ -1,0 +1,124 @@
+"""Calls on another stream than the current one that make their outputs (and
+workspaces) themselves: the memory comes from the launch stream's pool, so that no
+work queued on the current stream still uses it."""
+
+import pytest
+import torch
+
+import paged_kv_cache_473_b200 as pa
+from tests import draft_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+D, HQ, HKV, BLOCK = 64, 8, 2, 16
+LENS = [40, 7, 133]
+
+
+@pytest.fixture(autouse=True)
+def _clear_device_errors():
+    pa.device_errors()
+    yield
+    assert pa.device_errors() == 0
+
+
+def _pool_of(t):
+    """The stream whose pool a tensor's memory is from."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not torch's memory")
+
+
+def _inputs(dtype):
+    g = torch.Generator().manual_seed(4)
+    kc, vc, tables, cl = ref.pool(g, LENS, HKV, D, BLOCK, dtype, fill=0.0)
+    s = {"kc": kc, "vc": vc, "tables": tables, "cl": cl, "max": max(LENS)}
+    B = len(LENS)
+
+    def rows(*shape):
+        return torch.randn((*shape, D), generator=g).to(dtype).cuda()
+
+    s["q"], s["qt"], s["k"], s["v"] = rows(B, HQ), rows(B, 5, HQ), rows(B, HKV), rows(B, HKV)
+    s["mask"] = ref.random_trees(g, B, 5)[0].cuda()
+    s["pos"] = (cl - 1).contiguous()
+    s["inv"] = torch.rand(D // 2, generator=g).cuda()
+    s["slots"] = torch.full((B,), -1, dtype=torch.int64).cuda()
+    s["slots"][1] = int(tables[1, 0]) * BLOCK + 6
+    s["accepted"] = torch.tensor([[0, 1]] * B, dtype=torch.int32).cuda()
+    s["take"] = torch.full((B,), 2, dtype=torch.int32).cuda()
+    s["cu"] = torch.arange(B + 1, dtype=torch.int32).cuda()
+    return s
+
+
+def _norm_rope(s, stream):
+    return pa.qk_norm_rope(s["q"], s["k"], s["pos"], s["inv"], stream=stream)
+
+
+def _append(s, stream):
+    kc, vc = s["kc"].clone(), s["vc"].clone()  # (rows of padding tokens are not written)
+    torch.cuda.current_stream().synchronize()
+    out = pa.rope_append(s["q"], s["k"], s["v"], s["pos"], s["slots"], s["inv"], kc, vc, stream=stream)
+    torch.cuda.synchronize()
+    return out[1:2]
+
+
+def _tree(s, stream):
+    return pa.decode_tree(s["qt"], s["kc"], s["vc"], s["tables"], s["cl"], s["mask"], D ** -0.5,
+                          max_context_len=s["max"], stream=stream)
+
+
+def _commit(s, stream):
+    return pa.commit_tree(s["kc"], s["vc"], s["tables"], s["cl"], s["accepted"], s["take"], tree_len=5, stream=stream)
+
+
+DRAFT = [_norm_rope, _append, _tree, _commit]
+
+
+def _check(call, dtype):
+    s = _inputs(dtype)
+    want = call(s, None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, torch.cuda.ExternalStream(side.cuda_stream)):
+        out = call(s, stream)
+        side.synchronize()
+        for got, w in zip(out if isinstance(out, tuple) else (out,), want if isinstance(want, tuple) else (want,)):
+            assert _pool_of(got) == side.cuda_stream
+            assert torch.equal(got, w)
+    with torch.cuda.stream(side):  # the current stream: its own pool, as ever
+        out = call(s, None)
+        assert _pool_of(out[0] if isinstance(out, tuple) else out) == side.cuda_stream
+    with torch.cuda.stream(side):  # and the default stream, by its handle, from another one
+        out = call(s, 0)
+    torch.cuda.synchronize()
+    for got, w in zip(out if isinstance(out, tuple) else (out,), want if isinstance(want, tuple) else (want,)):
+        assert _pool_of(got) == 0 and torch.equal(got, w)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("call", DRAFT)
+def test_outputs_of_the_drafting_step(call, dtype):
+    _check(call, dtype)
+
+
+@pytest.mark.parametrize("call", [_norm_rope, _tree])
+def test_an_output_is_not_given_away_while_the_current_stream_uses_it(call):
+    """Dropped by the caller with its use queued on the current stream, its memory is not reused before that has run."""
+    s = _inputs(torch.bfloat16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = call(s, side)
+    out = out[0] if isinstance(out, tuple) else out
+    side.synchronize()
+    at, want = out.data_ptr(), out.clone()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # the current stream is busy for a tenth of a second
+    copy = out.clone()
+    shape, dtype = out.shape, out.dtype
+    del out
+    with torch.cuda.stream(side):
+        other = torch.empty(shape, dtype=dtype, device="cuda")
+        assert other.data_ptr() != at
+        other.zero_()
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
