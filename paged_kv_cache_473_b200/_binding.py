@@ -174,6 +174,27 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream, device, make, returned: bool = True) -> torch.Tensor:
+    """A new tensor that a call uses on ``stream`` (the current one when None): made there, from
+    that stream's memory, which work queued on another stream no longer uses.  One that the
+    caller gets is not given to others while the current stream, where it may be used next, still does."""
+    if stream is None:
+        return make()
+    current, handle = torch.cuda.current_stream(device), _stream(stream)
+    if handle == current.cuda_stream:
+        return make()
+    on = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(on):
+        t = make()
+    if returned:
+        t.record_stream(current)
+    return t
+
+
+def _zeroed_workspace(need: int, q: torch.Tensor, stream) -> torch.Tensor:
+    return _on_stream(stream, q.device, lambda: torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device), False)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
         return None
@@ -196,11 +217,11 @@ def write_kv(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cac
     _check(st, "pa_write_kv")
 
 
-def _decode_common(q, k_cache, block_tables, out):
+def _decode_common(q, k_cache, block_tables, out, stream):
     B, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _on_stream(stream, q.device, lambda: torch.empty_like(q))
     return B, hq, d, nb, hkv, bs, out
 
 
@@ -208,7 +229,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
            context_lens: torch.Tensor, scale: float, softcap: float = 0.0, window: int = 0,
            out: Optional[torch.Tensor] = None, kernel: str = "auto", stream=None) -> torch.Tensor:
     """Paged decode attention, one CTA per (sequence, kv head).  Returns ``out``."""
-    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out)
+    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out, stream)
     st = _lib().pa_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), B, hq, hkv, d,
                        bs, block_tables.shape[1], nb, float(scale), float(softcap), int(window), _ptr(out),
                        _dtype_code(q), KERNELS[kernel], _stream(stream))
@@ -238,10 +259,10 @@ def decode_splitk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     zero-filled before its first use; it is allocated zeroed with torch if not
     given.
     """
-    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out)
+    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out, stream)
     if workspace is None:  # (a given workspace's size is checked by the library)
         need = decode_splitk_workspace_size(B, hq, d, max_context_len, partition_tokens, hkv)
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _zeroed_workspace(need, q, stream)
     wbytes = workspace.numel() * workspace.element_size()
     st = _lib().pa_decode_splitk(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), B, hq,
                               hkv, d, bs, block_tables.shape[1], nb, float(scale), float(softcap), int(window),
@@ -265,10 +286,10 @@ def decode_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """Split-K decode where sequences ``0 .. n_sharers-1`` share their first
     ``prefix_len`` positions (same blocks): the prefix is read once per kv head
     for all of them, then merged with each sequence's own range."""
-    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out)
+    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out, stream)
     need = decode_cascade_workspace_size(B, hq, d, max_context_len, prefix_len, partition_tokens, hkv)
     if workspace is None:
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _zeroed_workspace(need, q, stream)
     wbytes = workspace.numel() * workspace.element_size()
     st = _lib().pa_decode_cascade(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), B, hq,
                                hkv, d, bs, block_tables.shape[1], nb, float(scale), float(softcap), int(window),
@@ -290,7 +311,7 @@ def decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cac
     with the combine (``max_context_len`` required; workspace allocated with
     torch if not given).
     """
-    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out)
+    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out, stream)
     ptoks = int(partition_tokens) if split else -1
     wptr, wbytes = None, 0
     if split:
@@ -298,7 +319,7 @@ def decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cac
             raise ValueError("decode_step(split=True) needs max_context_len")
         if workspace is None:  # (a given workspace's size is checked by the library)
             need = decode_splitk_workspace_size(B, hq, d, max_context_len, partition_tokens, hkv)
-            workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+            workspace = _zeroed_workspace(need, q, stream)
         wptr, wbytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     st = _lib().pa_decode_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                             _ptr(context_lens), B, hq, hkv, d, bs, block_tables.shape[1], nb, float(scale),
@@ -329,7 +350,7 @@ def decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     B, T, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _on_stream(stream, q.device, lambda: torch.empty_like(q))
     ptoks = int(partition_tokens) if split else -1
     wptr, wbytes = None, 0
     if split:
@@ -337,7 +358,7 @@ def decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             raise ValueError("decode_multi(split=True) needs max_context_len")
         need = decode_multi_workspace_size(B, T, hq, d, max_context_len, partition_tokens, hkv)
         if workspace is None:
-            workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+            workspace = _zeroed_workspace(need, q, stream)
         wptr, wbytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     st = _lib().pa_decode_multi(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), B, T, hq,
                              hkv, d, bs, block_tables.shape[1], nb, float(scale), float(softcap), int(window),
@@ -358,7 +379,7 @@ def prefill(q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torc
     total, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _on_stream(stream, q.device, lambda: torch.empty_like(q))
     st = _lib().pa_prefill(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(cu_q_lens), total,
                         int(max_q_len), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
                         cu_q_lens.numel() - 1, hq, hkv, d, bs, block_tables.shape[1], nb, float(scale),
@@ -572,7 +593,7 @@ def decode_splitk_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     """``decode_splitk`` for callers that must not allocate device memory: the
     split-K scratch is the library's own fixed array, and ``out`` must be given.
     Calls must not overlap on the GPU (they share that array)."""
-    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out)
+    B, hq, d, nb, hkv, bs, out = _decode_common(q, k_cache, block_tables, out, stream)
     st = _lib().pa_decode_splitk_noalloc(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
                                       B, hq, hkv, d, bs, block_tables.shape[1], nb, float(scale), float(softcap),
                                       int(window), _ptr(out), _dtype_code(q), int(partition_tokens),

@@ -71,6 +71,44 @@ def _commit(s, stream):
     return pa.commit_tree(s["kc"], s["vc"], s["tables"], s["cl"], s["accepted"], s["take"], tree_len=5, stream=stream)
 
 
+def _args(s, q="q"):
+    return s[q], s["kc"], s["vc"], s["tables"], s["cl"], D ** -0.5
+
+
+def _decode(s, stream):
+    return pa.decode(*_args(s), stream=stream)
+
+
+def _splitk(s, stream):
+    return pa.decode_splitk(*_args(s), max_context_len=s["max"], stream=stream)
+
+
+def _splitk_parts(s, stream):
+    return pa.decode_splitk(*_args(s), max_context_len=s["max"], partition_tokens=64, stream=stream)
+
+
+def _step(s, stream):
+    kc, vc = s["kc"].clone(), s["vc"].clone()
+    torch.cuda.current_stream().synchronize()
+    out = pa.decode_step(s["q"], s["k"], s["v"], kc, vc, s["tables"], s["cl"], D ** -0.5, max_context_len=s["max"],
+                         stream=stream)
+    torch.cuda.synchronize()
+    return out
+
+
+def _multi(s, stream):
+    return pa.decode_multi(*_args(s, "qt"), max_context_len=s["max"], stream=stream)
+
+
+def _cascade(s, stream):
+    return pa.decode_cascade(*_args(s), n_sharers=0, prefix_len=0, max_context_len=s["max"], stream=stream)
+
+
+def _prefill(s, stream):
+    return pa.prefill(s["q"], None, None, None, s["cu"], s["kc"], s["vc"], s["tables"], s["cl"], D ** -0.5, max_q_len=1,
+                      stream=stream)
+
+
 DRAFT = [_norm_rope, _append, _tree, _commit]
 
 
@@ -101,7 +139,31 @@ def test_outputs_of_the_drafting_step(call, dtype):
     _check(call, dtype)
 
 
-@pytest.mark.parametrize("call", [_norm_rope, _tree])
+@pytest.mark.parametrize("dtype,call", [(torch.float32, c) for c in (_decode, _splitk, _splitk_parts)] +
+                         [(torch.bfloat16, c) for c in (_decode, _splitk, _splitk_parts, _step, _multi, _cascade, _prefill)])
+def test_outputs_of_the_other_calls(dtype, call):
+    _check(call, dtype)
+
+
+@pytest.mark.parametrize("call", [_splitk, _splitk_parts, _multi, _step])
+def test_a_workspace_is_zero_where_the_call_runs(call):
+    """With the current stream busy, and memory that is not zero in the launch stream's pool."""
+    s = _inputs(torch.bfloat16)
+    want = call(s, None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        held = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (1 << 10, 1 << 16, 1 << 20, 8 << 20)]
+    side.synchronize()
+    del held
+    if call is not _step:  # (which waits for the current stream before the call)
+        torch.cuda._sleep(100_000_000)
+    out = call(s, side)
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("call", [_norm_rope, _tree, _splitk])
 def test_an_output_is_not_given_away_while_the_current_stream_uses_it(call):
     """Dropped by the caller with its use queued on the current stream, its memory is not reused before that has run."""
     s = _inputs(torch.bfloat16)
