@@ -327,8 +327,9 @@ size_t pa_decode_cascade_workspace_size(int32_t batch, int32_t num_q_heads, int3
  *               rotary_dim on are not rotated; rotary_dim = 0: norm only
  *               (positions and inv_freq may be NULL).
  *   q_out, k_out: as q and k, with their own strides; q_out == q and k_out ==
- *   k with equal strides work in place (any other overlap is undefined).  The
- *   results are pa_decode_step's q and k_new, or pa_prefill's.
+ *   k with equal strides work in place (with others, more than one token is
+ *   PA_ERR_INVALID; any other overlap is undefined).  The results are
+ *   pa_decode_step's q and k_new, or pa_prefill's.
  *   positions: int32 [num_tokens], any value.
  *   Supported: head_dim in {64, 128, 256}; rotary_dim a multiple of 16 in
  *   [0, head_dim]; any head counts (num_q_heads need not divide by
@@ -355,7 +356,8 @@ pa_status_t pa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
  *     k_cache[s / bs][h][s % bs][:] = rotated k[i][h][:],
  *     v_cache[s / bs][h][s % bs][:] = v[i][h][:],   s = slot_mapping[i].
  *   q_out: [num_tokens][num_q_heads][head_dim], contiguous; q_out == q works
- *   in place when q_stride is num_q_heads * head_dim.
+ *   in place when q_stride is num_q_heads * head_dim (PA_ERR_INVALID with
+ *   another stride and more than one token).
  *   slot_mapping[i] < 0 marks a padding token: neither its q_out row nor the
  *   cache is written.  A slot >= num_blocks * block_size sets PA_DEVERR_SLOT;
  *   its K and V rows are skipped, its q_out row is written.  Two tokens with

@@ -79,6 +79,7 @@ pa_status_t check_norm_rope(const NormRopeParams& p, int32_t num_tokens, int32_t
   if (!p.q || !p.k || !p.q_out || !aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(p.q_out, 16)) return PA_ERR_INVALID;
   if (p.q_stride < 0 || p.k_stride < 0 || p.q_stride % step || p.k_stride % step) return PA_ERR_INVALID;
   if (p.q_out_stride < (int64_t)p.hq * head_dim || p.q_out_stride % step) return PA_ERR_INVALID;
+  if (p.q_out == p.q && p.q_out_stride != p.q_stride && num_tokens > 1) return PA_ERR_INVALID;
   if (!aligned(p.q_weight, 16) || !aligned(p.k_weight, 16)) return PA_ERR_INVALID;
   if (p.rotary > 0 && (!p.positions || !p.inv_freq)) return PA_ERR_INVALID;
   if (!aligned(p.positions, 4) || !aligned(p.inv_freq, 4)) return PA_ERR_INVALID;
@@ -251,7 +252,7 @@ pa_status_t pa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int6
   const pa_status_t st = check_norm_rope(p, num_tokens, head_dim, dtype, &empty);
   if (st != PA_OK || empty) return st;
   if (!k_out || !aligned(k_out, 16) || k_out_stride < (int64_t)num_kv_heads * head_dim ||
-      k_out_stride % (dtype == PA_F32 ? 4 : 8))
+      k_out_stride % (dtype == PA_F32 ? 4 : 8) || (k_out == k && k_out_stride != k_stride && num_tokens > 1))
     return PA_ERR_INVALID;
   if (launch_norm_rope<false>(p, num_tokens, head_dim, dtype, stream) != cudaSuccess) return PA_ERR_CUDA;
   pa_host::set_last_launches(1);
