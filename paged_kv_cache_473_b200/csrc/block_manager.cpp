@@ -6,13 +6,28 @@
 #include "../../include/block_manager.h"
 
 #include <cstring>
-#include <deque>
 #include <new>
 #include <unordered_map>
 #include <unordered_set>
 #include <vector>
 
 namespace {
+
+// Block ids, first in, first out.  Room for every block is taken at the start, so
+// that giving blocks back allocates nothing and cannot fail.
+struct FreeList {
+  std::vector<int32_t> ids;
+  size_t first = 0, count = 0;
+
+  bool empty() const { return count == 0; }
+  void push(int32_t id) { ids[(first + count++) % ids.size()] = id; }
+  int32_t pop() {
+    const int32_t id = ids[first];
+    first = (first + 1) % ids.size();
+    --count;
+    return id;
+  }
+};
 
 constexpr uint64_t kNoHash = 0;
 
@@ -57,7 +72,7 @@ struct Seq {
 struct pa_block_manager {
   int32_t num_blocks = 0, block_size = 0;
   std::vector<Block> blocks;
-  std::deque<int32_t> free_list;  // blocks with count 0, in the order they were freed (stale entries skipped)
+  FreeList free_list;             // blocks with count 0, in the order they were freed (stale entries skipped), each once
   std::vector<char> in_free;      // block is in free_list
   int32_t n_free = 0;
   std::unordered_map<uint64_t, int32_t> cache;  // hash -> registered block
@@ -97,8 +112,7 @@ struct pa_block_manager {
   // Take a free block (count 0 -> 1); the caller has checked n_free > 0.
   int32_t allocate() {
     while (!free_list.empty()) {
-      const int32_t id = free_list.front();
-      free_list.pop_front();
+      const int32_t id = free_list.pop();
       in_free[id] = 0;
       if (blocks[id].ref != 0) continue;  // revived from the prefix cache since it was freed
       unregister(id);
@@ -118,7 +132,7 @@ struct pa_block_manager {
     if (--blocks[id].ref == 0) {
       ++n_free;
       if (!in_free[id]) {
-        free_list.push_back(id);
+        free_list.push(id);
         in_free[id] = 1;
       }
     }
@@ -191,7 +205,8 @@ pa_block_manager* pa_bm_create(int32_t num_blocks, int32_t block_size) {
     bm->block_size = block_size;
     bm->blocks.resize(num_blocks);
     bm->in_free.assign(num_blocks, 1);
-    for (int32_t i = 0; i < num_blocks; ++i) bm->free_list.push_back(i);
+    bm->free_list.ids.resize(num_blocks);
+    for (int32_t i = 0; i < num_blocks; ++i) bm->free_list.push(i);
     bm->n_free = num_blocks;
   } catch (...) {
     delete bm;
@@ -258,18 +273,23 @@ pa_status_t pa_bm_append_slots(pa_block_manager* bm, const int64_t* seq_ids, con
   if (!bm || n < 0 || (n > 0 && (!seq_ids || !slots_out || !cow_out || !num_cow))) return PA_ERR_INVALID;
   const int32_t bs = bm->block_size;
   // Check everything first: ids known and distinct, and enough free blocks
-  // for the new blocks and copies the step needs.
+  // for the new blocks and copies the step needs (and host memory for their ids).
   int32_t need = 0;
-  std::unordered_set<int64_t> seen;
-  for (int32_t i = 0; i < n; ++i) {
-    auto it = bm->seqs.find(seq_ids[i]);
-    if (it == bm->seqs.end() || !seen.insert(seq_ids[i]).second) return PA_ERR_INVALID;
-    const Seq& s = it->second;
-    if (s.len % bs == 0) {
-      ++need;  // a new block
-    } else if (bm->blocks[s.blocks.back()].ref > 1) {
-      ++need;  // copy-on-write of the shared partial last block
+  try {
+    std::unordered_set<int64_t> seen;
+    for (int32_t i = 0; i < n; ++i) {
+      auto it = bm->seqs.find(seq_ids[i]);
+      if (it == bm->seqs.end() || !seen.insert(seq_ids[i]).second) return PA_ERR_INVALID;
+      Seq& s = it->second;
+      if (s.len % bs == 0) {
+        ++need;  // a new block
+        if (s.blocks.size() == s.blocks.capacity()) s.blocks.reserve(2 * s.blocks.size() + 1);
+      } else if (bm->blocks[s.blocks.back()].ref > 1) {
+        ++need;  // copy-on-write of the shared partial last block
+      }
     }
+  } catch (...) {
+    return PA_ERR_INVALID;  // out of host memory
   }
   if (need > bm->n_free) return PA_ERR_WORKSPACE;
   int32_t ncow = 0;
