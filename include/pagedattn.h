@@ -400,7 +400,12 @@ pa_status_t pa_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   zero rows.
  *   A chain of drafts (word j = the bits 0 .. j) is pa_decode_multi.
  *   1 <= tree_len <= 64 (PA_ERR_UNSUPPORTED above).  bf16 runs on the tensor
- *   cores, fp32 on CUDA cores.
+ *   cores, fp32 on CUDA cores.  Scores, maxima and sums are fp32; for bf16 each
+ *   weight is rounded to bf16 for its product with V (2^-8 of it at most), as in
+ *   the other bf16 calls.  The same call gives the same bits.  The order of a
+ *   row's sums depends on how the work is cut, which follows from the lengths of
+ *   the whole batch (bf16) or from max_context_len (fp32): a sequence may come
+ *   out rounded otherwise in another batch or under another bound.
  *   workspace: for bf16, device memory of at least
  *   pa_decode_tree_workspace_size() bytes, 16-byte aligned.  Its first
  *   PA_COUNTER_BYTES, where pa_decode_splitk's family counts, are left as they

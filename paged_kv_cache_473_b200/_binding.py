@@ -7,6 +7,9 @@ kernels.  torch provides device memory (the optional ``out`` tensors and the
 split-K workspace) and streams.  The binding refuses to run if the library is
 missing or cannot be built; there is no fallback path.
 
+``stream``: what a call allocates (an ``out`` that is not given, a workspace) is made
+on the launch stream.  The caller orders its own tensors between streams.
+
 The library is opened on first use (the first call, or the first read of
 ``lib``), not at import, so that importing the package for its input
 generators (``workloads``) maps no GPU code.
@@ -453,8 +456,11 @@ def decode_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     ``tree_mask``: int64 ``[B, T]``, or ``[T]`` for one tree that every sequence
     drafts; bit i of node j's word says that j attends node i (its ancestors and
     itself).  ``tree_lens`` (int32 ``[B]``): nodes of each sequence's tree, when
-    they have fewer than T (the rows of the others are zero).  The workspace
-    (allocated with torch if not given) may be one that ``decode_splitk`` uses too.
+    they have fewer than T (the rows of the others are zero).  Up to 8 query heads
+    per kv head, as in the other calls; on bf16 caches the softmax's weights are
+    rounded to bf16 for their product with V.  The workspace (allocated with torch if
+    not given) may be one that ``decode_splitk`` uses too, and one sized for the
+    largest tree serves the smaller ones.
     """
     return (_native_module or _native()).decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, scale,
                                                      softcap, window, max_context_len, tree_lens, out, workspace,

@@ -17,9 +17,9 @@
 //     run beside the other's; each group sums its own weights.
 //   PAIR (two row tiles, head_dim 64 and 128): each group has a row tile and an O
 //     of its own, and both use every tile, so K and V come to the SM once for 256
-//     rows.  (Two CTAs with a row tile each, as before, read them twice and were
-//     bound by that: 8 trees of 64 over 16K-128K keys 583 us, every byte
-//     twice from DRAM.)
+//     rows.  (Two CTAs with a row tile each read them twice, every byte from DRAM:
+//     8 trees of 64 over 16K-128K keys 655 us where pairs took 636, before the
+//     steps below.)
 //
 // Split.  The units, in order, are one line of work: of each, a fixed cost (its Q,
 // masks and rows, counted in tiles) and its tiles.  The line is cut into one range
@@ -29,7 +29,7 @@
 // is cut are written as partials, at most two per range (the piece that comes
 // from the range before, the one that goes on in the next), and joined by
 // tree_combine_kernel.  (The line's last 3/16 in shorter ranges, claimed by CTAs that
-// are done: 538 for 495 us on 8 trees of 64 over 16K-128K keys, 124 for 113 on 256 of
+// are done: 554 for 510 us on 8 trees of 64 over 16K-128K keys, 125 for 114 on 256 of
 // 24: a claimed range costs its CTA more, some 5 us, than SMs differ.)
 //
 // Warps 0-7: softmax, one row per thread; they also write the rows.  Warp 11: MMA

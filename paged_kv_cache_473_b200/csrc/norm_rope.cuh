@@ -23,13 +23,15 @@
 // passes between lanes, and a lane reads and writes only its own elements
 // (which makes in-place calls safe).  Issue slots come next to DRAM (72 % of them
 // used before the arithmetic was packed), so it goes two elements to an instruction.
-// B200, append of 16384 tokens of 48 rows of 128, bf16: 68 us, 0.90 of the copy rate;
+// B200, append of 16384 tokens of 48 rows of 128, bf16: 68 us on the machine of the
+// comparisons below, 0.90 of the copy rate (72, 0.86, on another);
 // 74 one element at a time; with 6, 9 or 10 CTAs an SM 72, 70 and 78; three rows in
 // flight 71, six (at 6 CTAs) 69; the sums of four rows taken together, with fewer
 // shuffles, 84 (a row then waits for the others); with eight neighbouring elements
 // a lane and the pairs' other halves by shuffles 83.  The token's rotary / 2 angles
-// are computed once, two or so a lane, and pass through shared memory; a lane sits
-// at the same place of each of its rows and keeps the four it needs in registers.
+// are computed by each warp that has rows of it, two or so a lane, and pass through
+// shared memory; a lane sits at the same place of each of its rows and keeps the
+// four it needs in registers.
 #pragma once
 
 #include "decode_common.cuh"

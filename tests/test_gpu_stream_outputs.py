@@ -184,3 +184,27 @@ def test_an_output_is_not_given_away_while_the_current_stream_uses_it(call):
         other.zero_()
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("call", [_norm_rope, _tree, _commit, _splitk_parts, _multi])
+def test_outputs_on_a_forked_stream_of_a_capture(call):
+    """Captured on a stream that joins the current one; an output that is kept, and one that is dropped."""
+    s = _inputs(torch.bfloat16)
+    want = call(s, None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        current = torch.cuda.current_stream()
+        side.wait_stream(current)
+        call(s, side)
+        out = call(s, side)
+        current.wait_stream(side)
+    for _ in range(2):
+        for x in out if isinstance(out, tuple) else (out,):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip(out if isinstance(out, tuple) else (out,), want if isinstance(want, tuple) else (want,)):
+            assert torch.equal(got, w)
+    del graph, out
